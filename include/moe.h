@@ -352,6 +352,120 @@ int32_t moe_mx_dispatch_gemm1(const moe_shape* shape, const uint8_t* xq, const u
 int32_t moe_mx_gemm2_combine(const moe_shape* shape, const uint8_t* w2q, const uint8_t* w2s, const float* topk_w,
                              void* ws, size_t ws_bytes, uint16_t* y, void* stream);
 
+/*
+ * Operators around the expert layer: the row norm in front of it, the router that gives it
+ * topk_idx and topk_w, and its 4-bit form for the few tokens of a decode step.  Element types are
+ * passed as moe_dtype; a row of a 2-D operand marked with a leading dimension (ld*, in elements, at
+ * least the row's length) is contiguous, its rows need not be.
+ */
+typedef enum moe_dtype { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
+typedef enum moe_norm_kind { MOE_LAYER_NORM = 0, MOE_RMS_NORM = 1 } moe_norm_kind;
+typedef enum moe_score { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
+
+/*
+ * Row norm.  Per row of x, with mean = sum x / cols (layer norm; 0 for RMS norm) and
+ * rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps):  y = (x - mean) rstd weight + bias.
+ *   x, y         [device] dtype [rows, cols], leading dimensions ldx, ldy; y must not overlap x
+ *   weight, bias [device] wdtype [cols]; wdtype is dtype or MOE_FP32; either may be NULL (1 resp. 0);
+ *                RMS norm takes no bias (MOE_ERR_SHAPE)
+ *   mean, rstd   [device] fp32 [rows], written for the backward; either may be NULL; mean is not
+ *                written for RMS norm
+ * Statistics are fp32; a non-finite element makes its row non-finite.  rows >= 0 (0: nothing is done),
+ * cols 1 .. 32768, eps >= 0 (MOE_ERR_SHAPE otherwise).  Pointers need their element's alignment only.
+ */
+int32_t moe_norm_forward(int32_t kind, int32_t dtype, int32_t wdtype, int64_t rows, int32_t cols, const void* x, int64_t ldx,
+                         const void* weight, const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                         void* stream);
+
+/* Bytes of ws for moe_norm_backward (a pure function; 0 for invalid arguments). */
+size_t moe_norm_workspace_bytes(int32_t dtype, int64_t rows, int32_t cols);
+
+/*
+ * Backward of moe_norm_forward: with xh = (x - mean) rstd and g = dy weight,
+ *   dx      = rstd (g - [layer norm: sum g / cols] - xh sum (g xh) / cols)   dtype [rows, cols]
+ *   dweight = sum over the rows of dy xh,  dbias = sum over the rows of dy   wdtype [cols]
+ * summed in fp32 in an order that the sizes fix.  dx, dweight and dbias may each be NULL, not all; dbias
+ * is for layer norm only (MOE_ERR_SHAPE).  rows == 0 writes zeros to dweight and dbias.  mean (layer
+ * norm) and rstd as the forward wrote them.  ws [device], moe_norm_workspace_bytes bytes, 256-B
+ * aligned, is scratch; it may be NULL when neither dweight nor dbias is asked for.  dx must not overlap
+ * x or dy.
+ */
+int32_t moe_norm_backward(int32_t kind, int32_t dtype, int32_t wdtype, int64_t rows, int32_t cols, const void* dy, int64_t lddy,
+                          const void* x, int64_t ldx, const void* weight, const float* mean, const float* rstd, void* dx,
+                          int64_t lddx, void* dweight, void* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Router ("Mega MoE" page, Key points: the layer takes the routing as an input; this makes it).  Per
+ * row of logits [device] dtype [T, E] (leading dimension ld):
+ *   l = min(logit, largest fp32); an expert whose logit is NaN or -inf is out of service, as is one
+ *   whose score s = l + bias is NaN or -inf (bias [device] fp32 [E], may be NULL; it takes part in
+ *   the choice only).
+ *   n_group > 1: the experts form n_group equal groups of consecutive ids; the topk_group groups of
+ *   the largest sum of their two best scores stay (one expert in service: its score; ties: lower group).
+ *   topk_idx [device] int32 [T, k]: the k largest scores, descending, ties to the lower id; -1 in the
+ *   slots for which no expert is left (moe_route_prologue ignores such ids).
+ *   topk_w [device] fp32 [T, k]: scale * p, 0 in those slots, with p = exp(l) (MOE_SOFTMAX) divided by
+ *   its sum over the chosen experts (renormalize != 0) or over all in service, or p = 1 / (1 + exp(-l))
+ *   (MOE_SIGMOID), divided by its sum over the chosen (renormalize != 0) or not.
+ * T >= 0, E 1 .. 1024, k 1 .. min(32, E), n_group 1 .. 16 a divisor of E, topk_group 1 .. n_group.
+ */
+int32_t moe_route_topk(int32_t dtype, int32_t T, int32_t E, int32_t k, const void* logits, int64_t ld, const float* bias,
+                       int32_t score, int32_t renormalize, int32_t n_group, int32_t topk_group, float scale,
+                       int32_t* topk_idx, float* topk_w, void* stream);
+
+/*
+ * Gradient of topk_w with respect to the logits, for the choice that moe_route_topk made (topk_idx; the
+ * choice itself has no gradient, nor has bias): dlogits [device] dtype [T, E] (leading dimension ldd),
+ * every element written.  dtopk_w [device] fp32 [T, k]; slots with an id outside [0, E) are ignored.
+ * dlogits must not overlap logits.
+ */
+int32_t moe_route_topk_backward(int32_t dtype, int32_t T, int32_t E, int32_t k, const void* logits, int64_t ld,
+                                const int32_t* topk_idx, const float* dtopk_w, int32_t score, int32_t renormalize, float scale,
+                                void* dlogits, int64_t ldd, void* stream);
+
+/*
+ * 4-bit weights with group scales.  A matrix of N output columns and reduction length K, in groups of
+ * `group` (a power of two, at least 32, that divides K) consecutive k:
+ *   codes  [device] uint8 [N, K / 2]      code of (n, k) in nibble k % 2 (low first) of byte k / 2
+ *   scales [device] dtype [N, K / group]  dtype (MOE_BF16 or MOE_FP16) is that of the activations
+ *   zeros  [device] uint8 [N, K / group]  zero points 0 .. 15, or NULL: 8
+ * and weight (n, k) = (code - zero) * scale.  E matrices follow one another.  codes, scales and zeros
+ * are 16-byte aligned.  K is at most 32768.
+ *
+ * moe_w4_quantize makes them from w [device] wdtype [E, K, N] (the logical x @ W layout): zeros NULL:
+ * scale = max |w| / 7; else scale = (max(w, 0) - min(w, 0)) / 15 and zero = -min(w, 0) / scale rounded;
+ * the scale is rounded to dtype, the code is the nearest integer to w / scale + zero (ties to even)
+ * kept in 0 .. 15.  A group of zeros has scale 0.  The weights have to be finite.
+ */
+int32_t moe_w4_quantize(int32_t wdtype, int32_t dtype, int32_t E, int32_t K, int32_t N, int32_t group, const void* w,
+                        uint8_t* codes, void* scales, uint8_t* zeros, void* stream);
+
+/*
+ * y[m, n] = sum over k of x[m, k] * weight(n, k), for few rows (each 64 rows stream the weights once):
+ * x [device] dtype [M, K] (leading dimension ldx, a multiple of 8; 16-byte aligned), y [device] dtype
+ * [M, N] (ldy).  The codes are multiplied unscaled and summed in fp32; each group's scale enters in fp32.
+ * M 0 .. 1048576, N >= 1, K a multiple of group.  A non-finite activation makes its row of y non-finite.
+ */
+int32_t moe_w4_linear(int32_t dtype, int32_t M, int32_t N, int32_t K, int32_t group, const void* x, int64_t ldx,
+                      const uint8_t* codes, const void* scales, const uint8_t* zeros, void* y, int64_t ldy, void* stream);
+
+/* Bytes of ws for moe_forward_w4 (a pure function; 0 for an invalid shape). */
+size_t moe_w4_workspace_bytes(const moe_shape* shape);
+
+/*
+ * Expert layer on 4-bit weights, for the few tokens of a decode step: y as moe_forward defines it, from
+ * x [device] dtype [T, H] and
+ *   w1 codes, s1, z1: EL matrices of N = 2I columns (gate columns 0 .. I-1, then up), K = H
+ *   w2 codes, s2, z2: EL matrices of N = H columns, K = I       (z1, z2 may be NULL)
+ * SwiGLU is applied in fp32 and the activation rounded to dtype; L2 sums, weights and combines in fp32
+ * in slot order (the same bits on every run); y [device] dtype [T, H].  An expert's weights are read
+ * once per 16 of its pairs.  T * k at most 4096 (MOE_ERR_SHAPE): longer batches are for moe_forward and
+ * moe_forward_mx.  shape->train must be 0; block_m is not used.  ws [device] 256-B aligned scratch.
+ */
+int32_t moe_forward_w4(const moe_shape* shape, int32_t dtype, int32_t group, const void* x, const int32_t* topk_idx,
+                       const float* topk_w, const uint8_t* w1, const void* s1, const uint8_t* z1, const uint8_t* w2,
+                       const void* s2, const uint8_t* z2, void* ws, size_t ws_bytes, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,6 +13,7 @@ gradient, SwiGLU transpose, dW2 and dW1 with a variable K, L1 dgrad NN with its 
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -29,6 +30,8 @@ ENTRY_POINTS = (
     "moe_bwd_gemm1_dgrad_combine", "moe_wgrad2", "moe_wgrad1", "moe_backward",
     "moe_mx_cast_fp8", "moe_mx_pack_weights", "moe_forward_mx", "moe_mx_dispatch_gemm1",
     "moe_mx_gemm2_combine", "moe_forward_noalloc",
+    "moe_norm_forward", "moe_norm_workspace_bytes", "moe_norm_backward", "moe_route_topk",
+    "moe_route_topk_backward", "moe_w4_quantize", "moe_w4_linear", "moe_w4_workspace_bytes", "moe_forward_w4",
 )
 NOALLOC_SCRATCH_BYTES = 256 * 1024 * 1024   # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 
@@ -88,9 +91,18 @@ def lib():
         L.moe_forward_mx.argtypes = [S, P, P, P, P, P, P, P, P, ctypes.c_float, P, ctypes.c_size_t, P, P]
         L.moe_mx_dispatch_gemm1.argtypes = [S, P, P, P, P, ctypes.c_float, P, ctypes.c_size_t, P]
         L.moe_mx_gemm2_combine.argtypes = [S, P, P, P, P, ctypes.c_size_t, P, P]
+        i64, f32, size = ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+        L.moe_norm_forward.argtypes = [i32, i32, i32, i64, i32, P, i64, P, P, f32, P, i64, P, P, P]
+        L.moe_norm_workspace_bytes.argtypes = [i32, i64, i32]
+        L.moe_norm_backward.argtypes = [i32, i32, i32, i64, i32, P, i64, P, i64, P, P, P, P, i64, P, P, P, size, P]
+        L.moe_route_topk.argtypes = [i32, i32, i32, i32, P, i64, P, i32, i32, i32, i32, f32, P, P, P]
+        L.moe_route_topk_backward.argtypes = [i32, i32, i32, i32, P, i64, P, P, i32, i32, f32, P, i64, P]
+        L.moe_w4_quantize.argtypes = [i32, i32, i32, i32, i32, i32, P, P, P, P, P]
+        L.moe_w4_linear.argtypes = [i32, i32, i32, i32, i32, P, i64, P, P, P, P, i64, P]
+        L.moe_w4_workspace_bytes.argtypes = [S]
+        L.moe_forward_w4.argtypes = [S, i32, i32] + [P] * 10 + [size, P, P]
         for n in ENTRY_POINTS[2:]:
-            if n != "moe_workspace_bytes":
-                getattr(L, n).restype = i32
+            getattr(L, n).restype = size if n.endswith("workspace_bytes") else i32
         _lib = L
     return _lib
 
@@ -436,3 +448,301 @@ def moe_layer(x, topk_idx, topk_w, w1p, w2p, shape, ws=None):
     if ws is None:
         ws = alloc_workspace(shape, x.device)
     return _MoeLayer.apply(x, topk_w, w1p, w2p, topk_idx, shape, ws)
+
+
+# ------------------------------------------------------------------------------------------------
+# Operators around the expert layer: row norm, router, 4-bit products
+# ------------------------------------------------------------------------------------------------
+_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_KIND = {"layer": 0, "rms": 1}
+_SCORE = {"softmax": 0, "sigmoid": 1}
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _place(t, name, stream):
+    """Context in which t's device is the current one and `stream` (of that device) its stream, so that
+    what a call allocates and enqueues is placed where t is."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise MoeError("%s must be a tensor on a GPU" % name)
+    if stream is not None:
+        if stream.device != t.device:
+            raise MoeError("stream is on %s, %s on %s" % (stream.device, name, t.device))
+        return torch.cuda.stream(stream)
+    return _HERE_ALREADY if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _like(t, dtype, name, shape, like):
+    """Address of a contiguous tensor of this dtype and shape on like's device (None stays None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != like.device or not t.is_contiguous():
+        raise MoeError("%s must be a contiguous %s tensor on %s" % (name, dtype, like.device))
+    if t.shape != shape:
+        raise MoeError("%s has the shape %s; %s is needed" % (name, tuple(t.shape), tuple(shape)))
+    return t.data_ptr()
+
+
+def _code(table, key, name):
+    if key not in table:
+        raise MoeError("%s is %r; one of %s is needed" % (name, key, sorted(map(str, table))))
+    return table[key]
+
+
+def _row_stride(t):
+    """Elements from one row (last dimension) of t to the next where the rows are contiguous, evenly spaced
+    and apart, else None."""
+    cols = t.shape[-1]
+    if t.is_contiguous():
+        return cols
+    if t.stride(-1) != 1 and cols > 1:
+        return None
+    ld, step = None, None
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = st
+        elif st != step:
+            return None
+        step = st * n
+    return cols if ld is None else ld if ld >= cols else None
+
+
+def _rows(t, name, like=None, shape=None):
+    """(address, leading dimension, rows, columns) of a tensor seen as rows of its last dimension."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() < 1:
+        raise MoeError("%s must be a tensor of rows on a GPU" % name)
+    if like is not None and (t.device != like.device or t.dtype != like.dtype or t.shape != shape):
+        raise MoeError("%s must be %s of the shape %s on %s" % (name, like.dtype, tuple(shape), like.device))
+    cols = t.shape[-1]
+    if cols == 0:
+        raise MoeError("%s has rows of no element" % name)
+    ld = _row_stride(t)
+    if ld is None:
+        raise MoeError("%s must have contiguous rows, evenly spaced, that do not overlap" % name)
+    return t.data_ptr(), ld, t.numel() // cols, cols
+
+
+def _handle():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def norm_forward(x, weight=None, bias=None, eps=1e-5, kind="layer", y=None, stream=None):
+    """(y, mean, rstd) of the row norm of x over its last dimension (moe_norm_forward): kind "layer" or
+    "rms" (no bias; mean is None).  weight and bias in x's dtype or fp32.  mean and rstd fp32, one per row."""
+    with _place(x, "x", stream):
+        px, ldx, rows, cols = _rows(x, "x")
+        wd = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            py, ldy = y.data_ptr(), cols
+        else:
+            py, ldy = _rows(y, "y", x, x.shape)[:2]
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if kind == "layer" else None
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        _check(lib().moe_norm_forward(_code(_KIND, kind, "kind"), _code(_DTYPE, x.dtype, "x.dtype"), _code(_DTYPE, wd, "weight.dtype"), rows, cols,
+                                      px, ldx, _like(weight, wd, "weight", (cols,), x), _like(bias, wd, "bias", (cols,), x), eps, py, ldy,
+                                      mean.data_ptr() if mean is not None else None, rstd.data_ptr(), _handle()), "moe_norm_forward")
+    return y, mean, rstd
+
+
+def norm_backward(dy, x, weight, mean, rstd, kind="layer", bias=False, dx=True, stream=None):
+    """(dx, dweight, dbias) of norm_forward (moe_norm_backward); dweight is None without a weight, dbias
+    without bias (a truth value: whether its gradient is wanted), dx with dx=False."""
+    with _place(x, "x", stream):
+        px, ldx, rows, cols = _rows(x, "x")
+        pdy, lddy = _rows(dy, "dy", x, x.shape)[:2]
+        dt = _code(_DTYPE, x.dtype, "x.dtype")
+        wd = weight.dtype if weight is not None else x.dtype
+        gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx else None
+        gw = torch.empty(cols, dtype=wd, device=x.device) if weight is not None else None
+        gb = torch.empty(cols, dtype=wd, device=x.device) if bias else None
+        if gx is None and gw is None and gb is None:
+            return None, None, None
+        nbytes = int(lib().moe_norm_workspace_bytes(dt, rows, cols)) if gw is not None or gb is not None else 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+        p = lambda t: t.data_ptr() if t is not None else None
+        stats = x.shape[:-1]
+        _check(lib().moe_norm_backward(_code(_KIND, kind, "kind"), dt, _code(_DTYPE, wd, "weight.dtype"), rows, cols, pdy, lddy, px, ldx,
+                                       _like(weight, wd, "weight", (cols,), x), _like(mean, torch.float32, "mean", stats, x),
+                                       _like(rstd, torch.float32, "rstd", stats, x), p(gx), cols, p(gw), p(gb), p(ws), nbytes, _handle()),
+               "moe_norm_backward")
+    return gx, gw, gb
+
+
+def _row_major(t):
+    """t itself where its rows can be walked in place, else a contiguous copy (a gradient that autograd
+    expanded or transposed)."""
+    return t if _row_stride(t) is not None else t.contiguous()
+
+
+class _Norm(torch.autograd.Function):
+    """norm_forward, with norm_backward for the gradients of x, weight and bias."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, kind):
+        y, mean, rstd = norm_forward(x, weight, bias, eps, kind)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.kind, ctx.bias_dtype = kind, bias.dtype if bias is not None else None
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        gx, gw, gb = norm_backward(_row_major(dy), x, weight, mean, rstd, ctx.kind, bias=want[2], dx=want[0])
+        if gb is not None:
+            gb = gb.to(ctx.bias_dtype)   # another dtype only where there is no weight to set it
+        return gx, gw if want[1] else None, gb, None, None
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5):
+    """Layer norm over the last dimension of x (bf16, fp16 or fp32), differentiable in x, weight and bias.
+    x has contiguous, evenly spaced rows; weight and bias [cols] in x's dtype or fp32."""
+    return _Norm.apply(x, weight, bias, eps, "layer")
+
+
+def rms_norm(x, weight=None, eps=1e-5):
+    """x / sqrt(mean x^2 + eps) * weight over the last dimension, otherwise as layer_norm."""
+    return _Norm.apply(x, weight, None, eps, "rms")
+
+
+def route_topk(logits, k, bias=None, score="softmax", renormalize=True, n_group=1, topk_group=1, scale=1.0, topk_idx=None, topk_w=None,
+               stream=None):
+    """(topk_idx int32 [T, k], topk_w fp32 [T, k]) of router logits [T, E] (moe_route_topk): what moe_layer
+    and the forward entry points take as their routing.  `router` is the differentiable form."""
+    with _place(logits, "logits", stream):
+        if logits.dim() != 2:
+            raise MoeError("logits must be [T, E]")
+        p, ld, T, E = _rows(logits, "logits")
+        if topk_idx is None:
+            topk_idx = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+        if topk_w is None:
+            topk_w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+        _check(lib().moe_route_topk(_code(_DTYPE, logits.dtype, "logits.dtype"), T, E, k, p, ld, _like(bias, torch.float32, "bias", (E,), logits),
+                                    _code(_SCORE, score, "score"), bool(renormalize), n_group, topk_group, scale,
+                                    _like(topk_idx, torch.int32, "topk_idx", (T, k), logits), _like(topk_w, torch.float32, "topk_w", (T, k), logits),
+                                    _handle()), "moe_route_topk")
+    return topk_idx, topk_w
+
+
+def route_topk_backward(logits, topk_idx, dtopk_w, score="softmax", renormalize=True, scale=1.0, dlogits=None, stream=None):
+    """dlogits [T, E] of route_topk for the gradient dtopk_w [T, k] (moe_route_topk_backward)."""
+    with _place(logits, "logits", stream):
+        if logits.dim() != 2 or topk_idx.dim() != 2:
+            raise MoeError("logits must be [T, E] and topk_idx [T, k]")
+        p, ld, T, E = _rows(logits, "logits")
+        k = topk_idx.shape[1]
+        if dlogits is None:
+            dlogits = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
+        pd, ldd = _rows(dlogits, "dlogits", logits, logits.shape)[:2]
+        _check(lib().moe_route_topk_backward(_code(_DTYPE, logits.dtype, "logits.dtype"), T, E, k, p, ld, _like(topk_idx, torch.int32, "topk_idx", (T, k), logits),
+                                             _like(dtopk_w, torch.float32, "dtopk_w", (T, k), logits), _code(_SCORE, score, "score"),
+                                             bool(renormalize), scale, pd, ldd, _handle()), "moe_route_topk_backward")
+    return dlogits
+
+
+class _Router(torch.autograd.Function):
+    """route_topk, with route_topk_backward for the gradient of the logits."""
+
+    @staticmethod
+    def forward(ctx, logits, k, bias, score, renormalize, n_group, topk_group, scale):
+        idx, w = route_topk(logits, k, bias, score, renormalize, n_group, topk_group, scale)
+        ctx.save_for_backward(logits, idx)
+        ctx.how = score, renormalize, scale
+        ctx.mark_non_differentiable(idx)
+        return idx, w
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _, dw):
+        logits, idx = ctx.saved_tensors
+        return (route_topk_backward(logits, idx, dw.contiguous(), *ctx.how),) + (None,) * 7
+
+
+def router(logits, k, bias=None, score="softmax", renormalize=True, n_group=1, topk_group=1, scale=1.0):
+    """route_topk as an autograd op: (topk_idx, topk_w), topk_w differentiable in the logits.  Feeds
+    moe_layer, whose backward hands d(topk_w) back."""
+    return _Router.apply(logits, k, bias, score, renormalize, n_group, topk_group, scale)
+
+
+def w4_quantize(w, group=128, zeros=False, dtype=None, stream=None):
+    """(codes, scales, zeros or None) of weights w [E, K, N] or [K, N] in the x @ W layout (moe_w4_quantize):
+    uint8 [E, N, K / 2], dtype [E, N, K / group] and uint8 [E, N, K / group].  dtype, that of the
+    activations to come, is w's own, or bf16 for fp32 weights."""
+    with _place(w, "w", stream):
+        if w.dim() not in (2, 3) or not w.is_contiguous():
+            raise MoeError("w must be contiguous, [E, K, N] or [K, N]")
+        if dtype is None:
+            dtype = torch.bfloat16 if w.dtype == torch.float32 else w.dtype
+        lead, (K, N) = tuple(w.shape[:-2]), w.shape[-2:]
+        if group < 1 or K % group != 0:
+            raise MoeError("K = %d is not a multiple of the group %d" % (K, group))
+        codes = torch.empty(lead + (N, K // 2), dtype=torch.uint8, device=w.device)
+        scales = torch.empty(lead + (N, K // group), dtype=dtype, device=w.device)
+        points = torch.empty(lead + (N, K // group), dtype=torch.uint8, device=w.device) if zeros else None
+        _check(lib().moe_w4_quantize(_code(_DTYPE, w.dtype, "w.dtype"), _code(_DTYPE, dtype, "dtype"), lead[0] if lead else 1, K, N, group, w.data_ptr(),
+                                     codes.data_ptr(), scales.data_ptr(), points.data_ptr() if zeros else None, _handle()), "moe_w4_quantize")
+    return codes, scales, points
+
+
+def _w4(w, name, x, lead, N, K):
+    """Addresses of a (codes, scales, zeros) triple of N columns and reduction length K, and its group."""
+    codes, scales, zeros = w
+    if not isinstance(scales, torch.Tensor) or scales.dim() != len(lead) + 2 or scales.shape[-1] < 1 or K % scales.shape[-1] != 0:
+        raise MoeError("%s: scales must be [%sN, K / group]" % (name, "E, " * len(lead)))
+    groups = scales.shape[-1]
+    return (_like(codes, torch.uint8, name + " codes", lead + (N, K // 2), x), _like(scales, x.dtype, name + " scales", lead + (N, groups), x),
+            _like(zeros, torch.uint8, name + " zeros", lead + (N, groups), x), K // groups)
+
+
+def w4_linear(x, codes, scales, zeros=None, y=None, stream=None):
+    """y [..., N] = x [..., K] times the 4-bit weights (codes uint8 [N, K / 2], scales [N, K / group] in x's
+    dtype, zeros uint8 [N, K / group] or None), for few rows (moe_w4_linear)."""
+    with _place(x, "x", stream):
+        px, ldx, M, K = _rows(x, "x")
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+            raise MoeError("codes must be [N, K / 2]")
+        N = codes.shape[0]
+        pc, ps, pz, group = _w4((codes, scales, zeros), "w", x, (), N, K)
+        shape = x.shape[:-1] + (N,)
+        if y is None:
+            y = torch.empty(shape, dtype=x.dtype, device=x.device)
+            py, ldy = y.data_ptr(), N
+        else:
+            py, ldy = _rows(y, "y", x, shape)[:2]
+        _check(lib().moe_w4_linear(_code(_DTYPE, x.dtype, "x.dtype"), M, N, K, group, px, ldx, pc, ps, pz, py, ldy, _handle()), "moe_w4_linear")
+    return y
+
+
+def w4_workspace_bytes(shape: Shape) -> int:
+    n = int(lib().moe_w4_workspace_bytes(ctypes.byref(shape)))
+    if n == 0:
+        raise MoeError("invalid shape %r for moe_forward_w4 (T * k at most 4096, no training)" % (shape,))
+    return n
+
+
+def w4_alloc_workspace(shape: Shape, device="cuda") -> torch.Tensor:
+    return torch.empty(w4_workspace_bytes(shape), dtype=torch.uint8, device=device)
+
+
+def forward_w4(shape, x, topk_idx, topk_w, w1, w2, ws, y=None, stream=None):
+    """y [T, H] of the expert layer on 4-bit weights, for the few tokens of a decode step (moe_forward_w4): x
+    bf16 or fp16 [T, H]; w1 and w2 are (codes, scales, zeros or None) of w4_quantize for W1 [EL, H, 2I] and
+    W2 [EL, I, H], with one group size; ws is w4_alloc_workspace(shape)'s."""
+    with _place(x, "x", stream):
+        T, H, I, EL = shape.T, shape.H, shape.I, shape.EL
+        px = _like(x, x.dtype, "x", (T, H), x)
+        one, two = _w4(w1, "w1", x, (EL,), 2 * I, H), _w4(w2, "w2", x, (EL,), H, I)
+        if one[3] != two[3]:
+            raise MoeError("w1 and w2 have groups of %d and %d" % (one[3], two[3]))
+        if y is None:
+            y = torch.empty(T, H, dtype=x.dtype, device=x.device)
+        p, n = _ws(ws)
+        if ws.device != x.device:
+            raise MoeError("ws is on %s, x on %s" % (ws.device, x.device))
+        _check(lib().moe_forward_w4(ctypes.byref(shape), _code(_DTYPE, x.dtype, "x.dtype"), one[3], px,
+                                    _like(topk_idx, torch.int32, "topk_idx", (T, shape.k), x), _like(topk_w, torch.float32, "topk_w", (T, shape.k), x),
+                                    *one[:3], *two[:3], p, n, _like(y, x.dtype, "y", (T, H), x), _handle()), "moe_forward_w4")
+    return y

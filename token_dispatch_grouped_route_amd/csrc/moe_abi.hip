@@ -486,4 +486,181 @@ int32_t moe_forward_mx(const moe_shape* shape, const uint8_t* xq, const uint8_t*
     return launched(e);
 }
 
+// ---------------------------------------------------------------------------------------------
+// Operators around the expert layer: row norm, router, 4-bit products
+// ---------------------------------------------------------------------------------------------
+namespace {
+constexpr int kNormMaxCols = 32768, kW4MaxK = 32768;
+bool is_dtype(int32_t t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
+bool is_16bit(int32_t t) { return t == MOE_BF16 || t == MOE_FP16; }
+int elem_bytes(int32_t t) { return t == MOE_FP32 ? 4 : 2; }
+bool aligned_to(const void* p, int32_t t) { return (reinterpret_cast<uintptr_t>(p) & (elem_bytes(t) - 1u)) == 0; }
+
+int32_t check_norm(int32_t kind, int32_t dtype, int32_t wdtype, int64_t rows, int32_t cols) {
+    if ((kind != MOE_LAYER_NORM && kind != MOE_RMS_NORM) || !is_dtype(dtype) || (wdtype != dtype && wdtype != MOE_FP32)) return MOE_ERR_SHAPE;
+    if (rows < 0 || rows > (int64_t(1) << 40) || cols < 1 || cols > kNormMaxCols) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+// A leading dimension: at least the row, and row offsets that stay inside int64.
+bool bad_ld(int64_t ld, int64_t rows, int64_t cols) { return ld < cols || (rows > 1 && ld > (int64_t(1) << 61) / rows); }
+}  // namespace
+
+size_t moe_norm_workspace_bytes(int32_t dtype, int64_t rows, int32_t cols) {
+    if (check_norm(MOE_LAYER_NORM, dtype, dtype, rows, cols) != MOE_OK) return 0;
+    const size_t part = align_up(static_cast<size_t>(norm_bwd_slots(rows, cols, elem_bytes(dtype))) * cols * 4);
+    return 2 * (part > 0 ? part : kWsAlign);
+}
+
+int32_t moe_norm_forward(int32_t kind, int32_t dtype, int32_t wdtype, int64_t rows, int32_t cols, const void* x, int64_t ldx,
+                         const void* weight, const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                         void* stream) {
+    const int32_t st = check_norm(kind, dtype, wdtype, rows, cols);
+    if (st != MOE_OK) return st;
+    if (!(eps >= 0.0f) || bad_ld(ldx, rows, cols) || bad_ld(ldy, rows, cols) || (kind == MOE_RMS_NORM && bias)) return MOE_ERR_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (!x || !y) return MOE_ERR_NULL;
+    if (x == y) return MOE_ERR_SHAPE;   // not in place
+    if (!aligned_to(x, dtype) || !aligned_to(y, dtype) || !aligned_to(weight, wdtype) || !aligned_to(bias, wdtype) || !aligned4(mean) || !aligned4(rstd))
+        return MOE_ERR_ALIGN;
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    NormArgs a = {};
+    a.rows = rows, a.cols = cols, a.x = x, a.ldx = ldx, a.weight = weight, a.bias = bias, a.eps = eps, a.y = y, a.ldy = ldy;
+    a.mean = mean, a.rstd = rstd;
+    return launched(launch_norm_fwd(a, dtype, wdtype, kind == MOE_LAYER_NORM, static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_norm_backward(int32_t kind, int32_t dtype, int32_t wdtype, int64_t rows, int32_t cols, const void* dy, int64_t lddy,
+                          const void* x, int64_t ldx, const void* weight, const float* mean, const float* rstd, void* dx,
+                          int64_t lddx, void* dweight, void* dbias, void* ws, size_t ws_bytes, void* stream) {
+    const int32_t st = check_norm(kind, dtype, wdtype, rows, cols);
+    if (st != MOE_OK) return st;
+    const bool layer = kind == MOE_LAYER_NORM;
+    if (bad_ld(ldx, rows, cols) || bad_ld(lddy, rows, cols) || (dx && bad_ld(lddx, rows, cols)) || (!layer && dbias)) return MOE_ERR_SHAPE;
+    if (!dx && !dweight && !dbias) return MOE_ERR_NULL;
+    if (rows > 0 && (!x || !dy || !rstd || (layer && !mean))) return MOE_ERR_NULL;
+    if (rows > 0 && (dx == x || dx == dy)) return MOE_ERR_SHAPE;   // not in place
+    if (!aligned_to(x, dtype) || !aligned_to(dy, dtype) || !aligned_to(dx, dtype) || !aligned_to(weight, wdtype) || !aligned_to(dweight, wdtype) ||
+        !aligned_to(dbias, wdtype) || !aligned4(mean) || !aligned4(rstd))
+        return MOE_ERR_ALIGN;
+    NormArgs a = {};
+    if (dweight || dbias) {
+        if (!ws) return MOE_ERR_NULL;
+        if ((reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) != 0) return MOE_ERR_ALIGN;
+        const size_t need = moe_norm_workspace_bytes(dtype, rows, cols);
+        if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+        if (dweight) a.part_w = static_cast<float*>(ws);
+        if (dbias) a.part_b = reinterpret_cast<float*>(static_cast<char*>(ws) + need / 2);
+    } else if (rows == 0) {
+        return MOE_OK;
+    }
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    a.rows = rows, a.cols = cols, a.x = x, a.ldx = ldx, a.dy = dy, a.lddy = lddy, a.weight = weight, a.y = dx, a.lddx = lddx;
+    a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd), a.dweight = dweight, a.dbias = dbias;
+    return launched(launch_norm_bwd(a, dtype, wdtype, layer, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+int32_t check_route(int32_t dtype, int32_t T, int32_t E, int32_t k, int64_t ld, int32_t score) {
+    if (!is_dtype(dtype) || T < 0 || E < 1 || E > 1024 || k < 1 || k > 32 || k > E || bad_ld(ld, T, E)) return MOE_ERR_SHAPE;
+    return score == MOE_SOFTMAX || score == MOE_SIGMOID ? MOE_OK : MOE_ERR_SHAPE;
+}
+}  // namespace
+
+int32_t moe_route_topk(int32_t dtype, int32_t T, int32_t E, int32_t k, const void* logits, int64_t ld, const float* bias,
+                       int32_t score, int32_t renormalize, int32_t n_group, int32_t topk_group, float scale,
+                       int32_t* topk_idx, float* topk_w, void* stream) {
+    const int32_t st = check_route(dtype, T, E, k, ld, score);
+    if (st != MOE_OK) return st;
+    if (n_group < 1 || n_group > 16 || E % n_group != 0 || topk_group < 1 || topk_group > n_group) return MOE_ERR_SHAPE;
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_idx || !topk_w) return MOE_ERR_NULL;
+    if (!aligned_to(logits, dtype) || !aligned4(bias) || !aligned4(topk_idx) || !aligned4(topk_w)) return MOE_ERR_ALIGN;
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    RouteArgs a = {};
+    a.T = T, a.E = E, a.k = k, a.n_group = n_group, a.topk_group = topk_group, a.sigmoid = score == MOE_SIGMOID;
+    a.renorm = renormalize != 0, a.scale = scale, a.logits = logits, a.ld = ld, a.bias = bias, a.idx_out = topk_idx, a.w_out = topk_w;
+    return launched(launch_route_topk(a, dtype, false, static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_route_topk_backward(int32_t dtype, int32_t T, int32_t E, int32_t k, const void* logits, int64_t ld,
+                                const int32_t* topk_idx, const float* dtopk_w, int32_t score, int32_t renormalize, float scale,
+                                void* dlogits, int64_t ldd, void* stream) {
+    const int32_t st = check_route(dtype, T, E, k, ld, score);
+    if (st != MOE_OK) return st;
+    if (bad_ld(ldd, T, E)) return MOE_ERR_SHAPE;
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_idx || !dtopk_w || !dlogits) return MOE_ERR_NULL;
+    if (logits == dlogits) return MOE_ERR_SHAPE;   // not in place
+    if (!aligned_to(logits, dtype) || !aligned_to(dlogits, dtype) || !aligned4(topk_idx) || !aligned4(dtopk_w)) return MOE_ERR_ALIGN;
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    RouteArgs a = {};
+    a.T = T, a.E = E, a.k = k, a.sigmoid = score == MOE_SIGMOID, a.renorm = renormalize != 0, a.scale = scale;
+    a.logits = logits, a.ld = ld, a.idx = topk_idx, a.dw = dtopk_w, a.dlogits = dlogits, a.ldd = ldd;
+    return launched(launch_route_topk(a, dtype, true, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+// log2 of a group size that divides K, or -1.
+int group_shift(int32_t group, int32_t K) {
+    if (group < 32 || (group & (group - 1)) != 0 || K <= 0 || K > kW4MaxK || K % group != 0) return -1;
+    return __builtin_ctz(static_cast<unsigned>(group));
+}
+// Byte offsets of the act and stage rows of moe_forward_w4, and the total; false for a bad shape.
+bool w4_layout(const moe_shape* s, size_t* stage, size_t* total) {
+    if (check_shape(s) != MOE_OK || s->train || static_cast<int64_t>(s->T) * s->k > kW4MaxPairs) return false;
+    const size_t pairs = static_cast<size_t>(s->T) * s->k;
+    *stage = align_up(pairs * s->I * 2);
+    *total = *stage + align_up(pairs * s->H * 4) + kWsAlign;
+    return true;
+}
+}  // namespace
+
+int32_t moe_w4_quantize(int32_t wdtype, int32_t dtype, int32_t E, int32_t K, int32_t N, int32_t group, const void* w,
+                        uint8_t* codes, void* scales, uint8_t* zeros, void* stream) {
+    if (!is_dtype(wdtype) || !is_16bit(dtype) || E < 1 || E > 65535 || N < 1 || group_shift(group, K) < 0) return MOE_ERR_SHAPE;
+    if (!w || !codes || !scales) return MOE_ERR_NULL;
+    if (!aligned_to(w, wdtype) || !aligned16(codes) || !aligned16(scales) || !aligned16(zeros)) return MOE_ERR_ALIGN;
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    return launched(launch_w4_quantize(wdtype, dtype, E, K, N, group, w, codes, scales, zeros, static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_w4_linear(int32_t dtype, int32_t M, int32_t N, int32_t K, int32_t group, const void* x, int64_t ldx,
+                      const uint8_t* codes, const void* scales, const uint8_t* zeros, void* y, int64_t ldy, void* stream) {
+    const int gshift = group_shift(group, K);
+    if (!is_16bit(dtype) || M < 0 || M > (1 << 20) || N < 1 || N > (1 << 28) || gshift < 0 || bad_ld(ldx, M, K) || bad_ld(ldy, M, N)) return MOE_ERR_SHAPE;
+    if (M == 0) return MOE_OK;
+    if (!x || !codes || !scales || !y) return MOE_ERR_NULL;
+    if (!aligned16(x) || ldx % 8 != 0 || !aligned16(codes) || !aligned16(scales) || !aligned16(zeros) || !aligned_to(y, dtype)) return MOE_ERR_ALIGN;
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    const W4Linear a{M, N, K, gshift, x, ldx, ldy, codes, scales, zeros, y};
+    return launched(launch_w4_linear(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_w4_workspace_bytes(const moe_shape* shape) {
+    size_t stage, total;
+    return w4_layout(shape, &stage, &total) ? total : 0;
+}
+
+int32_t moe_forward_w4(const moe_shape* shape, int32_t dtype, int32_t group, const void* x, const int32_t* topk_idx,
+                       const float* topk_w, const uint8_t* w1, const void* s1, const uint8_t* z1, const uint8_t* w2,
+                       const void* s2, const uint8_t* z2, void* ws, size_t ws_bytes, void* y, void* stream) {
+    const int32_t st = check_shape(shape);
+    if (st != MOE_OK) return st;
+    size_t stage, total;
+    if (!w4_layout(shape, &stage, &total) || !is_16bit(dtype) || group_shift(group, shape->H) < 0 || group_shift(group, shape->I) < 0)
+        return MOE_ERR_SHAPE;
+    if (!w1 || !s1 || !w2 || !s2 || !ws || ((!x || !topk_idx || !topk_w || !y) && shape->T > 0)) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(w1) || !aligned16(s1) || !aligned16(z1) || !aligned16(w2) || !aligned16(s2) || !aligned16(z2) ||
+        !aligned16(y) || !aligned4(topk_idx) || !aligned4(topk_w) || (reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) != 0)
+        return MOE_ERR_ALIGN;
+    if (ws_bytes < total) return MOE_ERR_WORKSPACE;
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    W4Experts a = {};
+    a.T = shape->T, a.H = shape->H, a.I = shape->I, a.e_lo = shape->e_lo, a.EL = shape->EL, a.k = shape->k;
+    a.gshift = group_shift(group, shape->H), a.x = x, a.topk_idx = topk_idx, a.topk_w = topk_w;
+    a.w1 = w1, a.s1 = s1, a.z1 = z1, a.w2 = w2, a.s2 = s2, a.z2 = z2;
+    a.act = ws, a.stage = reinterpret_cast<float*>(static_cast<char*>(ws) + stage), a.y = y;
+    return launched(launch_w4_forward(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

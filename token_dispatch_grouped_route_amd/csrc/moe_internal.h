@@ -176,6 +176,65 @@ hipError_t launch_mx_gemm2(const Dims& d, const uint8_t* w2q, const uint8_t* w2s
 hipError_t launch_mx_pack(const Dims& d, const uint16_t* w1, const uint16_t* w2, uint8_t* w1q, uint8_t* w1s,
                           uint8_t* w2q, uint8_t* w2s, hipStream_t s);
 
+// Row norm (moe_norm_forward / moe_norm_backward): y is dx in the backward.
+struct NormArgs {
+    int64_t rows;
+    int32_t cols;
+    const void *x, *dy, *weight, *bias;
+    int64_t ldx, lddy, ldy, lddx;
+    float eps;
+    void *y, *dweight, *dbias;
+    float *mean, *rstd;
+    float *part_w, *part_b;   // [slots, cols] partial rows of dweight and dbias
+};
+int64_t norm_bwd_slots(int64_t rows, int cols, int elem_bytes);
+hipError_t launch_norm_fwd(const NormArgs& a, int dtype, int wdtype, bool layer, hipStream_t s);
+hipError_t launch_norm_bwd(const NormArgs& a, int dtype, int wdtype, bool layer, hipStream_t s);
+
+// Top-k router (moe_route_topk / moe_route_topk_backward).
+struct RouteArgs {
+    int32_t T, E, k, n_group, topk_group;
+    bool sigmoid, renorm;
+    float scale;
+    const void* logits;
+    const float* bias;
+    int64_t ld, ldd;
+    int32_t* idx_out;
+    float* w_out;
+    const int32_t* idx;
+    const float* dw;
+    void* dlogits;
+};
+hipError_t launch_route_topk(const RouteArgs& a, int dtype, bool backward, hipStream_t s);
+
+// 4-bit products (moe_w4_linear) and the expert layer on them (moe_forward_w4).
+struct W4Linear {
+    int32_t M, N, K, gshift;   // group = 1 << gshift
+    const void* x;
+    int64_t ldx, ldy;
+    const uint8_t* codes;
+    const void* scales;
+    const uint8_t* zeros;
+    void* y;
+};
+struct W4Experts {
+    int32_t T, H, I, e_lo, EL, k, gshift;
+    const void* x;
+    const int32_t* topk_idx;
+    const float* topk_w;
+    const uint8_t *w1, *z1, *w2, *z2;
+    const void *s1, *s2;
+    void* act;      // [T * k, I] in x's type, one row per pair
+    float* stage;   // [T * k, H] weighted L2 rows
+    void* y;
+    int32_t list_at;   // byte offset of the pair list in LDS (set at the launch)
+};
+constexpr int kW4MaxPairs = 4096;   // T * k of moe_forward_w4
+hipError_t launch_w4_linear(const W4Linear& a, int dtype, hipStream_t s);
+hipError_t launch_w4_forward(const W4Experts& a, int dtype, hipStream_t s);
+hipError_t launch_w4_quantize(int wdtype, int dtype, int E, int K, int N, int group, const void* w, uint8_t* codes, void* scales,
+                              uint8_t* zeros, hipStream_t s);
+
 // Compute units of the current device (cached per device).
 int device_cu_count();
 
