@@ -442,7 +442,7 @@ int32_t moe_w4_quantize(int32_t wdtype, int32_t dtype, int32_t E, int32_t K, int
 
 /*
  * y[m, n] = sum over k of x[m, k] * weight(n, k), for few rows (each 64 rows stream the weights once):
- * x [device] dtype [M, K] (leading dimension ldx, a multiple of 8; 16-byte aligned), y [device] dtype
+ * x [device] dtype [M, K] (leading dimension ldx, a multiple of 8 up to 2^23; 16-byte aligned), y [device] dtype
  * [M, N] (ldy).  The codes are multiplied unscaled and summed in fp32; each group's scale enters in fp32.
  * M 0 .. 1048576, N >= 1, K a multiple of group.  A non-finite activation makes its row of y non-finite.
  */

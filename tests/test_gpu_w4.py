@@ -68,7 +68,8 @@ def check_linear(x, w4, y=None, **kw):
 @pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("M,N,K,group", [(1, 1, 32, 32), (1, 100, 256, 128), (2, 17, 96, 32), (3, 64, 160, 32), (16, 33, 192, 64), (17, 130, 1024, 128), (5, 48, 4096, 256),
-                                         (33, 31, 512, 64), (64, 256, 1408, 128), (65, 40, 640, 32), (130, 20, 320, 64), (1, 4096, 7168, 128), (7, 50, 32768, 32)])
+                                         (33, 31, 512, 64), (64, 256, 1408, 128), (65, 40, 640, 32), (130, 20, 320, 64), (1, 4096, 7168, 128), (7, 50, 32768, 32),
+                                         (20, 10000, 256, 64), (3, 11000, 128, 32), (70, 5000, 384, 128), (2, 33000, 64, 32), (2, 33000, 32768, 32)])
 def test_linear(M, N, K, group, zeros, dtype):
     g = gen(M * 1000 + N)
     check_linear(torch.randn(M, K, generator=g, device="cuda").to(dtype), random_w4(g, (), N, K, group, dtype, zeros))
@@ -243,15 +244,23 @@ def test_experts_without_tokens():
     assert y.shape == (0, 256)
 
 
-def test_a_token_in_and_out_of_a_batch():
-    """A token's output has the same bits alone and in a batch (sums do not depend on the other rows)."""
-    s, x, idx, tw, w1, w2 = experts_inputs(24, 512, 256, 16, 16, 4, 64, torch.bfloat16, True)
-    y = moe.forward_w4(s, x, idx, tw, w1, w2, moe.w4_alloc_workspace(s))
-    one = moe.make_shape(1, 512, 256, 16, 16, 4, block_m=64)
-    ws = moe.w4_alloc_workspace(one)
-    for t in (0, 7, 23):
-        alone = moe.forward_w4(one, x[t:t + 1], idx[t:t + 1].contiguous(), tw[t:t + 1].contiguous(), w1, w2, ws)
-        assert torch.equal(alone[0], y[t])
+def test_tokens_do_not_reach_each_other():
+    """A token's output keeps its bits when the other tokens change, to NaN too, in both grids."""
+    for T in (3, 24):
+        s, x, idx, tw, w1, w2 = experts_inputs(T, 512, 256, 16, 16, 4, 64, torch.bfloat16, True)
+        ws = moe.w4_alloc_workspace(s)
+        y = moe.forward_w4(s, x, idx, tw, w1, w2, ws)
+        for fill in (1.0, float("nan")):
+            z = torch.full_like(x, fill)
+            z[1] = x[1]
+            assert torch.equal(moe.forward_w4(s, z, idx, tw, w1, w2, ws)[1], y[1])
+
+
+@pytest.mark.parametrize("T", [1, 20])
+@pytest.mark.parametrize("H,I", [(32768, 128), (128, 32768)])
+def test_experts_with_the_longest_reductions(H, I, T):
+    """As many scales as fit no workgroup of several teams."""
+    check_experts(*experts_inputs(T, H, I, 4, 2, 2, 32, torch.bfloat16, True))
 
 
 def test_large_weight_offsets():

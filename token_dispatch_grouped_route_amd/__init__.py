@@ -524,7 +524,8 @@ def _rows(t, name, like=None, shape=None):
 
 
 def _handle():
-    return torch.cuda.current_stream().cuda_stream
+    """The current stream of the current device (without the Stream object, which takes 3 us to make)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def norm_forward(x, weight=None, bias=None, eps=1e-5, kind="layer", y=None, stream=None):

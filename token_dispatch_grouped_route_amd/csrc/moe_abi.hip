@@ -491,6 +491,7 @@ int32_t moe_forward_mx(const moe_shape* shape, const uint8_t* xq, const uint8_t*
 // ---------------------------------------------------------------------------------------------
 namespace {
 constexpr int kNormMaxCols = 32768, kW4MaxK = 32768;
+constexpr int64_t kW4MaxLd = 1 << 23;   // 64 rows of x stay within 32-bit byte offsets
 bool is_dtype(int32_t t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
 bool is_16bit(int32_t t) { return t == MOE_BF16 || t == MOE_FP16; }
 int elem_bytes(int32_t t) { return t == MOE_FP32 ? 4 : 2; }
@@ -628,6 +629,7 @@ int32_t moe_w4_linear(int32_t dtype, int32_t M, int32_t N, int32_t K, int32_t gr
                       const uint8_t* codes, const void* scales, const uint8_t* zeros, void* y, int64_t ldy, void* stream) {
     const int gshift = group_shift(group, K);
     if (!is_16bit(dtype) || M < 0 || M > (1 << 20) || N < 1 || N > (1 << 28) || gshift < 0 || bad_ld(ldx, M, K) || bad_ld(ldy, M, N)) return MOE_ERR_SHAPE;
+    if (ldx > kW4MaxLd) return MOE_ERR_SHAPE;
     if (M == 0) return MOE_OK;
     if (!x || !codes || !scales || !y) return MOE_ERR_NULL;
     if (!aligned16(x) || ldx % 8 != 0 || !aligned16(codes) || !aligned16(scales) || !aligned16(zeros) || !aligned_to(y, dtype)) return MOE_ERR_ALIGN;

@@ -41,14 +41,16 @@ template <> struct W4Type<fp16_t> {   // 16.0 = 0x4c00, 10 mantissa bits: the ni
     }
 };
 
-// Eight codes (one dword, low nibble first) as 16 + q, in the order 0 4 1 5 2 6 3 7.
-template <typename T> __device__ __forceinline__ u32x4_t expand8(uint32_t w) {
-    using W = W4Type<T>;
+// Eight codes (one dword, low nibble first) as 16 + q, in the order 0 4 1 5 2 6 3 7: one shift and one
+// bit-field insert per two codes.  mask and base are W4Type's constants, held in registers (the
+// insert takes no literals).
+template <typename T> __device__ __forceinline__ u32x4_t expand8(uint32_t w, uint32_t mask, uint32_t base) {
     u32x4_t r;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        const int up = W::kBit - 4 * p;   // nibble p (and p + 4, 16 bits higher) to bit kBit
-        r[p] = ((up >= 0 ? w << up : w >> -up) & W::kMask) | W::kBase;
+        const int up = W4Type<T>::kBit - 4 * p;   // nibble p (and p + 4, 16 bits higher) to bit kBit
+        const uint32_t v = up >= 0 ? w << up : w >> -up;
+        r[p] = (v & mask) | (base & ~mask);
     }
     return r;
 }
@@ -74,148 +76,242 @@ __device__ __forceinline__ void transpose_groups(u32x4_t& d) {
 }
 
 constexpr int kW4Chunk = 128;   // k per wave and step
-constexpr int kW4Ahead = 4;     // chunks of weights in flight per wave
+constexpr int kW4Ahead = 2;     // steps in flight per wave
 
-// The sums of this wave's K chunks (wave, wave + WAVES, ...): sum[t][n][i] of x row 16 t + 4 (lane / 16) + i
-// and weight row lane % 16 of tile n.  wrow[n]: this lane's weight row (lane % 16) of tile n; xrow[t]: its x
-// row (lane % 16) of row tile t, or null; scales, zeros: LDS, this lane's row of tile n at n * 16 * groups.
-// FLUSH: MFMAs per scale (min(group, 128) / 32); gshift: log2 of the group.
-template <typename T, int MT, int NT, int FLUSH, bool ZEROS, int WAVES>
-__device__ __forceinline__ void w4_sums(const uint8_t* const (&wrow)[NT], const T* const (&xrow)[MT], const T* scales,
-                                        const uint8_t* zeros, int K, int gshift, f32x4_t (&sum)[MT][NT]) {
+// Weights and x are read through buffers, whose loads return 0 past the end: an offset of kNoRow or
+// kNoK or more (also of both added) lies past every buffer, none of which exceeds 2^30 bytes.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+constexpr uint32_t kNoRow = 0x80000000u, kNoK = 0x40000000u;
+__device__ __forceinline__ rsrc_t buffer_of(const void* p, int64_t bytes) {   // the same for the whole wave
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)), hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(static_cast<uint64_t>(hi) << 32 | lo), 0,
+                                             __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(bytes)), 0x00020000);
+}
+__device__ __forceinline__ u32x4_t load16(rsrc_t r, uint32_t at) {
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+}
+
+// Scales and zero points of a workgroup's NT tiles in LDS: a row per weight row, of `stride` elements, an
+// odd multiple of 8, so that the 16 rows a wave reads at once start in different banks.
+__host__ __device__ inline int w4_stride(int groups) { return ((groups + 7) / 8 | 1) * 8; }
+template <int NT, bool ZEROS> __host__ __device__ inline int w4_meta_bytes(int groups) { return 16 * NT * w4_stride(groups) * (ZEROS ? 3 : 2); }
+
+// What a wave multiplies: the weight rows of its NT tiles (codes: a buffer of one tile's rows each; wrow:
+// this lane's offset, row lane % 16 and K part lane / 16), and up to 16 rows of x (this lane's offset in
+// row w4_row(); kNoRow: no row).
+template <int NT> struct W4Operands {
+    rsrc_t codes[NT], x;
+    uint32_t wrow, xrow;
+    int K, gshift;
+};
+// The x row of a lane: row r is the MFMA's row 4 (r % 4) + r / 4, so that up to four rows all come out in
+// the first accumulator register of the lanes.
+__device__ __forceinline__ int w4_row() { return (threadIdx.x & 3) * 4 + ((threadIdx.x >> 2) & 3); }
+
+// The sums of this wave's K chunks (slice, slice + KS, ...): sum[n][i] of x row 4 i + lane / 16 and weight
+// row lane % 16 of tile n; with FEW (at most four rows) only i = 0.  kW4Ahead chunks are in flight; ready()
+// is called once the first are: it fills the LDS rows that scales and zeros (16 + z) point into, this
+// lane's row of tile 0.  FLUSH: MFMAs per scale (min(group, 128) / 32).  ORDERED: x is stored in expand8's
+// order within every 8 elements.
+template <typename T, int NT, int FLUSH, bool ZEROS, int KS, bool ORDERED, bool FEW, typename F>
+__device__ __forceinline__ void w4_sums(const W4Operands<NT>& o, int slice, const uint16_t* scales, const uint8_t* zeros, f32x4_t (&sum)[NT], F&& ready) {
     using W = W4Type<T>;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, part = lane >> 4;
-    const int groups = K >> gshift, chunks = (K + kW4Chunk - 1) / kW4Chunk;
+    const int K = o.K, tile = 16 * w4_stride(K >> o.gshift), chunks = (K + kW4Chunk - 1) / kW4Chunk;
     const u32x4_t ones = {W::kOnes, W::kOnes, W::kOnes, W::kOnes};
-    u32x4_t code[kW4Ahead][NT] = {};   // a lane group past K multiplies zero rows with whatever codes it holds
-    auto fetch = [&](int c, u32x4_t (&to)[NT]) {
-        const int k = c * kW4Chunk + 32 * part;
+    uint32_t mask = W::kMask, base = W::kBase;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(base));
+    u32x4_t code[kW4Ahead][NT], xs[kW4Ahead][4];
+    auto fetch = [&](int c, u32x4_t (&to)[NT], u32x4_t (&x)[4]) {
+        // k past K: zero rows of x (times the codes of whatever row lies there)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (k < K) to[n] = *reinterpret_cast<const u32x4_t*>(wrow[n] + (k >> 1));
+        for (int i = 0; i < 4; ++i) {
+            const int k = c * kW4Chunk + 32 * i;
+            x[i] = load16(o.x, o.xrow + (k < K ? 2 * static_cast<uint32_t>(k) : kNoK));
+        }
+        const uint32_t at = o.wrow + (c < chunks ? static_cast<uint32_t>(c) * (kW4Chunk / 2) : kNoRow);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) to[n] = load16(o.codes[n], at);
     };
 #pragma unroll
-    for (int u = 0; u < kW4Ahead; ++u) fetch(wave + u * WAVES, code[u]);
-
-    for (int c0 = wave; c0 < chunks; c0 += kW4Ahead * WAVES) {
+    for (int u = 0; u < kW4Ahead; ++u) fetch(slice + u * KS, code[u], xs[u]);
+    ready();
+    for (int c0 = slice; c0 < chunks; c0 += kW4Ahead * KS) {
 #pragma unroll
         for (int u = 0; u < kW4Ahead; ++u) {
-            const int c = c0 + u * WAVES, k0 = c * kW4Chunk;
-            if (c < chunks) {   // the same for the whole wave
-                u32x4_t xa[MT][4];
+            const int c = c0 + u * KS;
+            if (c >= chunks) break;   // the same for the whole wave
+            u32x4_t q[NT], xa[4];
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
+            for (int i = 0; i < 4; ++i) xa[i] = ORDERED ? xs[u][i] : order8(xs[u][i]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        xa[t][i] = u32x4_t{0, 0, 0, 0};
-                        if (xrow[t] && k0 + 32 * i < K) xa[t][i] = *reinterpret_cast<const u32x4_t*>(xrow[t] + k0 + 32 * i + 8 * part);
-                    }
-                u32x4_t q[NT];
+            for (int n = 0; n < NT; ++n) q[n] = code[u][n];
+            fetch(c + kW4Ahead * KS, code[u], xs[u]);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) q[n] = code[u][n];
-                fetch(c + kW4Ahead * WAVES, code[u]);
+            for (int n = 0; n < NT; ++n) transpose_groups(q[n]);
+            const int g = c * kW4Chunk >> o.gshift;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) transpose_groups(q[n]);
+            for (int f = 0; f < 4 / FLUSH; ++f) {   // groups past K multiply zero rows
+                f32x4_t sx = {}, acc[NT] = {};
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
+                for (int h = 0; h < FLUSH; ++h) {
+                    const int i = f * FLUSH + h;
+                    sx = W::mfma(xa[i], ones, sx);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) xa[t][i] = order8(xa[t][i]);
+                    for (int n = 0; n < NT; ++n) acc[n] = W::mfma(xa[i], expand8<T>(q[n][i], mask, base), acc[n]);
+                }
 #pragma unroll
-                for (int f = 0; f < 4 / FLUSH; ++f) {
-                    if (k0 + 32 * f * FLUSH >= K) break;
-                    f32x4_t sx[MT] = {}, acc[MT][NT] = {};
+                for (int n = 0; n < NT; ++n) {
+                    const float s = to_f32(__builtin_bit_cast(T, scales[n * tile + g + f]));
+                    const float z = ZEROS ? static_cast<float>(zeros[n * tile + g + f]) : 24.0f;
 #pragma unroll
-                    for (int h = 0; h < FLUSH; ++h) {   // MFMAs past K multiply zero rows
-                        const int i = f * FLUSH + h;
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) sx[t] = W::mfma(xa[t][i], ones, sx[t]);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const u32x4_t b = expand8<T>(q[n][i]);
-#pragma unroll
-                            for (int t = 0; t < MT; ++t) acc[t][n] = W::mfma(xa[t][i], b, acc[t][n]);
-                        }
-                    }
-                    const int g = (k0 + 32 * f * FLUSH) >> gshift;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float s = to_f32(scales[n * 16 * groups + g]);
-                        const float z = 16.0f + (ZEROS ? static_cast<float>(zeros[n * 16 * groups + g]) : 8.0f);
-#pragma unroll
-                        for (int t = 0; t < MT; ++t)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) sum[t][n][i] += s * (acc[t][n][i] - z * sx[t][i]);
-                    }
+                    for (int i = 0; i < (FEW ? 1 : 4); ++i) sum[n][i] += s * (acc[n][i] - z * sx[i]);
                 }
             }
         }
     }
 }
 
-// Copies `count` contiguous elements to LDS; src 16-byte aligned.
-template <typename E> __device__ __forceinline__ void stage(E* dst, const E* src, int count) {
-    constexpr int N = 16 / static_cast<int>(sizeof(E));
-    const int full = count / N;
-    for (int i = threadIdx.x; i < full; i += blockDim.x)
-        reinterpret_cast<u32x4_t*>(dst)[i] = reinterpret_cast<const u32x4_t*>(src)[i];
-    for (int i = full * N + threadIdx.x; i < count; i += blockDim.x) dst[i] = src[i];
-}
+// The scales and zero points of NT tiles on their way to LDS, for the KS waves that share the tiles: thread
+// i of them takes 8 groups, from group 8 (i / 16), of row i % 16 of every tile.  The loads are issued before the codes', so that the store
+// waits for them alone.  Groups beyond what one round of the waves covers follow in store().
+template <int NT, bool ZEROS, int KS> struct W4Meta {
+    static constexpr int kRound = 8 * 4 * KS;   // groups per round
+    static __device__ __forceinline__ int first() { return threadIdx.x % (64 * KS) >> 4 << 3; }
+    u32x4_t s[NT];
+    uint64_t z[NT];
+    const uint16_t* src[NT];    // first row of each tile
+    const uint8_t* zsrc[NT];
+    int rows[NT], groups;
 
-// LDS of a workgroup: scales and zero points of its NT tiles, and the waves' sums over them.
-template <int MT, int NT, int WAVES> size_t w4_lds_bytes(int groups, bool zeros) {
-    const size_t meta = static_cast<size_t>(16 * NT) * groups * (zeros ? 3 : 2), sums = static_cast<size_t>(WAVES) * MT * NT * 1024;
-    return (meta > sums ? meta : sums) + 16;
-}
-
-// Puts the waves' sums into LDS as [wave][t][n][lane][4] and calls f on them.
-template <int MT, int NT, int WAVES, typename F>
-__device__ __forceinline__ void w4_join(float* lds, const f32x4_t (&sum)[MT][NT], F&& f) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    __syncthreads();   // the scales are no longer read
+    __device__ __forceinline__ void load(int g) {
+        const int r = threadIdx.x & 15;
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+        for (int n = 0; n < NT; ++n) {
+            const int valid = r < rows[n] ? groups - g : 0;   // past the rows and groups: 0 (a NaN times a zero sum would stay)
+            s[n] = load_chunk<bf16_t>(reinterpret_cast<const bf16_t*>(src[n] + static_cast<int64_t>(r) * groups + g), valid);
+            z[n] = 0;
+            if constexpr (ZEROS) {
+                const uint8_t* p = zsrc[n] + static_cast<int64_t>(r) * groups + g;
+                typedef uint64_t u64_any __attribute__((aligned(1)));
+                if (valid >= 8) {
+                    z[n] = *reinterpret_cast<const u64_any*>(p);
+                } else {
+                    for (int i = 0; i < valid; ++i) z[n] |= static_cast<uint64_t>(p[i]) << (8 * i);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void load() { load(first()); }
+    __device__ __forceinline__ void store(uint16_t* scales, uint8_t* zeros) {
+        const int stride = w4_stride(groups), r = threadIdx.x & 15;
+        for (int g = first();;) {
+            if (g < stride) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    *reinterpret_cast<u32x4_t*>(scales + (16 * n + r) * stride + g) = s[n];
+                    if (ZEROS) *reinterpret_cast<uint64_t*>(zeros + (16 * n + r) * stride + g) = z[n] + 0x1010101010101010u;   // 16 + z
+                }
+            }
+            g += kRound;
+            if (g - first() >= stride) break;   // the same for all of them
+            load(g);
+        }
+    }
+};
+
+// A workgroup is TEAMS teams of KS waves; a team shares NT tiles and splits K.  LDS of a team: its scales and
+// zero points, then (in their place) its waves' sums.
+template <int NT, int KS, bool ZEROS> __host__ __device__ inline int w4_team_bytes(int groups) {
+    const int meta = w4_meta_bytes<NT, ZEROS>(groups), sums = KS > 1 ? KS * NT * 1024 : 0;
+    return ((meta > sums ? meta : sums) + 15) / 16 * 16;
+}
+
+// Orders a team's LDS accesses: nothing to wait for in a wave of its own.
+template <int KS> __device__ __forceinline__ void team_barrier() {
+    if constexpr (KS > 1) lds_barrier();
+    else __builtin_amdgcn_wave_barrier();
+}
+
+// f(m, col, values) for the elements of a team's tiles: row m, column col of each tile (values[n]).  The
+// waves' sums are added in wave order.
+template <int NT, int KS, typename F>
+__device__ __forceinline__ void w4_outputs(float* lds, int slice, const f32x4_t (&sum)[NT], F&& f) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (KS == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) v[n] = sum[n][i];
+            f(4 * i + (lane >> 4), lane & 15, v);
+        }
+    } else {
+        lds_barrier();   // the scales are no longer read
+#pragma unroll
+        for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4_t*>(lds + (slice * NT + n) * 256 + lane * 4) = sum[n];
+        lds_barrier();
+        for (int at = threadIdx.x % (64 * KS); at < 256; at += 64 * KS) {
+            const int m = at >> 4, col = at & 15;
+            float v[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float* p = lds + n * 256 + ((m & 3) * 16 + col) * 4 + (m >> 2);
+                v[n] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < KS; ++w) v[n] += p[w * NT * 256];
+            }
+            f(m, col, v);
+        }
+    }
+}
+
+// Grid: the 16-row tiles of x that share a workgroup's weights run on one XCD (workgroup b is on XCD b mod
+// 8), one after the other, so that all but the first read them from its L2.
+template <typename T, int NT, int FLUSH, bool ZEROS, int TEAMS, int KS, bool FEW>
+__global__ __launch_bounds__(64 * TEAMS * KS, 2) void w4_linear_kernel(W4Linear a) {
+    extern __shared__ __align__(16) unsigned char lds_raw[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), team = wave / KS, slice = wave % KS;
+    const int groups = a.K >> a.gshift, stride = w4_stride(groups);
+    const uint32_t row_tiles = (a.M + 15) / 16, b = blockIdx.x >> 3;
+    const int64_t col0 = (static_cast<int64_t>(b / row_tiles) * 8 + (blockIdx.x & 7)) * (16 * NT * TEAMS) + team * 16 * NT;
+    if (col0 - team * 16 * NT >= a.N) return;   // the whole workgroup
+    const int n0 = static_cast<int>(col0), m0 = static_cast<int>(b % row_tiles) * 16;
+    unsigned char* lds = lds_raw + team * w4_team_bytes<NT, KS, ZEROS>(groups);
+    uint16_t* scales = reinterpret_cast<uint16_t*>(lds);
+    uint8_t* zeros = lds + 16 * NT * stride * 2;
+
+    W4Operands<NT> o;
+    W4Meta<NT, ZEROS, KS> meta;
+    o.K = a.K;
+    o.gshift = a.gshift;
+    meta.groups = groups;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {   // rows past N read nothing
+        const int64_t row = n0 + 16 * n;
+        const int rows = max(0, min(16, a.N - static_cast<int>(row)));
+        meta.rows[n] = rows;
+        meta.src[n] = static_cast<const uint16_t*>(a.scales) + row * groups;
+        meta.zsrc[n] = ZEROS ? a.zeros + row * groups : nullptr;
+        o.codes[n] = buffer_of(a.codes + row * (a.K >> 1), rows * (a.K >> 1));
+    }
+    meta.load();
+    o.wrow = (lane & 15) * (a.K >> 1) + 16 * (lane >> 4);
+    o.x = buffer_of(static_cast<const T*>(a.x) + m0 * a.ldx, 2 * ((min(a.M - m0, 16) - 1) * a.ldx + a.K));
+    const int m = w4_row();
+    o.xrow = (m0 + m < a.M ? static_cast<uint32_t>(m * a.ldx * 2) : kNoRow) + 16 * (lane >> 4);
+    f32x4_t sum[NT] = {};
+    w4_sums<T, NT, FLUSH, ZEROS, KS, false, FEW>(o, slice, scales + (lane & 15) * stride, zeros + (lane & 15) * stride, sum, [&] {
+        meta.store(scales, zeros);
+        team_barrier<KS>();
+    });
+    w4_outputs<NT, KS>(reinterpret_cast<float*>(lds), slice, sum, [&](int r, int col, const float (&v)[NT]) {
+        if (m0 + r >= a.M) return;
+        T* y = static_cast<T*>(a.y) + (m0 + r) * a.ldy + n0 + col;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            *reinterpret_cast<f32x4_t*>(lds + ((wave * MT + t) * NT + n) * 256 + lane * 4) = sum[t][n];
-    __syncthreads();
-    f(lds);
-}
-// Element (row m, column n) of the tile (t, n) in a wave's sums.
-__device__ __forceinline__ int w4_at(int m, int n) { return ((m >> 2) * 16 + n) * 4 + (m & 3); }
-
-template <typename T, int MT, int NT, int FLUSH, bool ZEROS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void w4_linear_kernel(W4Linear a) {
-    extern __shared__ __align__(16) unsigned char lds_raw[];
-    const int lane = threadIdx.x & 63, groups = a.K >> a.gshift;
-    const int n0 = blockIdx.x * 16 * NT, m0 = blockIdx.y * 16 * MT, rows = min(16 * NT, a.N - n0);
-    T* scales = reinterpret_cast<T*>(lds_raw);
-    uint8_t* zeros = lds_raw + static_cast<size_t>(16 * NT) * groups * 2;
-    stage<uint16_t>(reinterpret_cast<uint16_t*>(scales), static_cast<const uint16_t*>(a.scales) + static_cast<int64_t>(n0) * groups, rows * groups);
-    if (ZEROS) stage<uint8_t>(zeros, a.zeros + static_cast<int64_t>(n0) * groups, rows * groups);
-    __syncthreads();
-
-    const uint8_t* wrow[NT];
-    const T* xrow[MT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)   // rows past N repeat the last one and are not stored
-        wrow[n] = a.codes + static_cast<int64_t>(min(n0 + 16 * n + (lane & 15), a.N - 1)) * (a.K >> 1);
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int m = m0 + 16 * t + (lane & 15);
-        xrow[t] = m < a.M ? static_cast<const T*>(a.x) + m * a.ldx : nullptr;
-    }
-    f32x4_t sum[MT][NT] = {};
-    w4_sums<T, MT, NT, FLUSH, ZEROS, WAVES>(wrow, xrow, scales + (lane & 15) * groups, zeros + (lane & 15) * groups, a.K, a.gshift, sum);
-    w4_join<MT, NT, WAVES>(reinterpret_cast<float*>(lds_raw), sum, [&](const float* part) {
-        for (int v = threadIdx.x; v < MT * NT * 256; v += 64 * WAVES) {
-            const int m = v / (16 * NT), n = v % (16 * NT);   // m in the row tiles, n in the columns of this workgroup
-            if (m0 + m >= a.M || n0 + n >= a.N) continue;
-            const float* p = part + ((m >> 4) * NT + (n >> 4)) * 256 + w4_at(m & 15, n & 15);
-            float s = 0.0f;
-#pragma unroll
-            for (int w = 0; w < WAVES; ++w) s += p[w * MT * NT * 256];
-            static_cast<T*>(a.y)[(m0 + m) * a.ldy + n0 + n] = from_f32<T>(s);
-        }
+            if (n0 + 16 * n + col < a.N) y[16 * n] = from_f32<T>(v[n]);
     });
 }
 
@@ -224,90 +320,88 @@ __global__ __launch_bounds__(64 * WAVES) void w4_linear_kernel(W4Linear a) {
 // of each expert works and the others leave; with more, one per local expert.  A workgroup lists its
 // expert's pairs in ascending order itself (the ids are a few KB), so no table is built beforehand.
 // ---------------------------------------------------------------------------------------------
-// The local expert of this workgroup row and its pairs (LDS list, count); false: nothing to do.
-__device__ __forceinline__ bool w4_pairs(const W4Experts& a, int* list, int* counts, int& expert, int& count) {
-    const int pairs = a.T * a.k, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    int first = 0, id;
-    if (pairs <= a.EL) {
-        first = blockIdx.y;
-        id = a.topk_idx[first];
-        if (id < a.e_lo || id >= a.e_lo + a.EL) return false;
-    } else {
-        id = a.e_lo + blockIdx.y;
-    }
-    expert = id - a.e_lo;
-    count = 0;
-    bool earlier = false;
-    for (int p0 = 0; p0 < pairs; p0 += blockDim.x) {
-        const int p = p0 + threadIdx.x;
+// The pairs of expert id, ascending, and their number; 0 if `first` >= 0 and an earlier pair has it.  Every
+// wave writes the whole list (the same values), so none waits for another.
+__device__ __forceinline__ int w4_pairs(const W4Experts& a, int id, int first, int* list) {
+    const int pairs = a.T * a.k, lane = threadIdx.x & 63;
+    int count = 0, earliest = pairs;
+    for (int p0 = 0; p0 < pairs; p0 += 64) {
+        const int p = p0 + lane;
         const bool mine = p < pairs && a.topk_idx[p] == id;
         const uint64_t m = __ballot(mine);
-        if (lane == 0) counts[wave] = __popcll(m);
-        __syncthreads();
-        int at = count;
-        for (int w = 0; w < waves; ++w) {
-            if (w == wave && mine) list[at + __popcll(m & ((uint64_t(1) << lane) - 1))] = p;
-            at += counts[w];
-        }
-        __syncthreads();
-        count = at;
+        if (mine) list[count + __popcll(m & ((uint64_t(1) << lane) - 1))] = p;
+        if (m != 0 && count == 0) earliest = p0 + __ffsll(static_cast<unsigned long long>(m)) - 1;
+        count += __popcll(m);
     }
-    if (pairs <= a.EL && count > 0) earlier = list[0] < first;
-    return count > 0 && !earlier;
+    __builtin_amdgcn_wave_barrier();   // the list is read by other lanes than those that wrote it
+    return earliest < first ? 0 : count;
 }
 
-// L1: NT = 2, tile 0 the gate columns 16 b .. and tile 1 the up columns of the same 16 intermediate
-// columns; act[pair] = silu(gate) up in T.  L2: NT tiles of output columns; stage[pair] = w o in fp32.
-template <typename T, bool L1, int NT, int FLUSH, bool ZEROS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void w4_experts_kernel(W4Experts a) {
+// L1: NT / 2 tiles of gate columns and as many of the up columns of the same intermediate columns;
+// act[pair] = silu(gate) up in T, in expand8's order.  L2: NT tiles of output columns; stage[pair] = w o in fp32.
+template <typename T, bool L1, int NT, int FLUSH, bool ZEROS, int TEAMS, int KS>
+__global__ __launch_bounds__(64 * TEAMS * KS, 2) void w4_experts_kernel(W4Experts a) {
     extern __shared__ __align__(16) unsigned char lds_raw[];
-    __shared__ int counts[WAVES];
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), team = wave / KS, slice = wave % KS;
+    const int pairs = a.T * a.k;
     int* list = reinterpret_cast<int*>(lds_raw + a.list_at);
-    int e, count;
-    if (!w4_pairs(a, list, counts, e, count)) return;
+    const bool by_pair = pairs <= a.EL;
+    const int id = by_pair ? __builtin_amdgcn_readfirstlane(a.topk_idx[blockIdx.y]) : a.e_lo + static_cast<int>(blockIdx.y), e = id - a.e_lo;
+    if (e < 0 || e >= a.EL) return;
+    const int count = w4_pairs(a, id, by_pair ? static_cast<int>(blockIdx.y) : -1, list);
+    if (count == 0) return;
 
-    const int K = L1 ? a.H : a.I, N = L1 ? 2 * a.I : a.H, groups = K >> a.gshift;
-    const int64_t wbase = static_cast<int64_t>(e) * N;   // rows of the expert
-    const uint8_t* codes = L1 ? a.w1 : a.w2;
-    const uint16_t* scale_g = static_cast<const uint16_t*>(L1 ? a.s1 : a.s2);
-    const uint8_t* zero_g = L1 ? a.z1 : a.z2;
-    T* scales = reinterpret_cast<T*>(lds_raw);
-    uint8_t* zeros = lds_raw + static_cast<size_t>(16 * NT) * groups * 2;
-    const uint8_t* wrow[NT];
+    const int K = L1 ? a.H : a.I, groups = K >> a.gshift, stride = w4_stride(groups);
+    constexpr int OUT = L1 ? 8 * NT : 16 * NT;   // output columns of a team: L1's first NT / 2 tiles are the gate's, the others the up's
+    const int col0 = (blockIdx.x * TEAMS + team) * OUT, columns = L1 ? a.I : a.H;
+    const int64_t wbase = static_cast<int64_t>(e) * (L1 ? 2 * a.I : a.H);   // first row of the expert
+    unsigned char* lds = lds_raw + team * w4_team_bytes<NT, KS, ZEROS>(groups);
+    uint16_t* scales = reinterpret_cast<uint16_t*>(lds);
+    uint8_t* zeros = lds + 16 * NT * stride * 2;
+    W4Operands<NT> o;
+    W4Meta<NT, ZEROS, KS> meta;
+    o.K = K;
+    o.gshift = a.gshift;
+    meta.groups = groups;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int col = col0 + 16 * (L1 ? n % (NT / 2) : n);
+        const int64_t row = wbase + col + (L1 && n >= NT / 2 ? a.I : 0);
+        const int rows = col < columns ? 16 : 0;   // the last team may hold tiles past the end (columns is a multiple of 16)
+        meta.rows[n] = rows;
+        meta.src[n] = static_cast<const uint16_t*>(L1 ? a.s1 : a.s2) + row * groups;
+        meta.zsrc[n] = ZEROS ? (L1 ? a.z1 : a.z2) + row * groups : nullptr;
+        o.codes[n] = buffer_of((L1 ? a.w1 : a.w2) + row * (K >> 1), rows * (K >> 1));
+    }
+    o.wrow = (lane & 15) * (K >> 1) + 16 * (lane >> 4);
+    o.x = buffer_of(L1 ? a.x : a.act, static_cast<int64_t>(L1 ? a.T : pairs) * (2 * K));
     for (int m0 = 0; m0 < count; m0 += 16) {
-        __syncthreads();   // the sums of the last rows are no longer read
+        meta.load();
+        const int m = m0 + w4_row();
+        o.xrow = (m < count ? static_cast<uint32_t>(L1 ? list[m] / a.k : list[m]) * (2 * K) : kNoRow) + 16 * (lane >> 4);
+        f32x4_t sum[NT] = {};
+        auto ready = [&] {
+            team_barrier<KS>();   // the sums of the last rows are no longer read
+            meta.store(scales, zeros);
+            team_barrier<KS>();
+        };
+        if (count - m0 <= 4) w4_sums<T, NT, FLUSH, ZEROS, KS, !L1, true>(o, slice, scales + (lane & 15) * stride, zeros + (lane & 15) * stride, sum, ready);
+        else w4_sums<T, NT, FLUSH, ZEROS, KS, !L1, false>(o, slice, scales + (lane & 15) * stride, zeros + (lane & 15) * stride, sum, ready);
+        w4_outputs<NT, KS>(reinterpret_cast<float*>(lds), slice, sum, [&](int r, int c, const float (&v)[NT]) {
+            if (m0 + r >= count) return;
+            const int pair = list[m0 + r];
+            if constexpr (L1) {
+                // column c goes where expand8's order has it: 0 4 1 5 2 6 3 7 -> c = 4 h + q at 2 q + h
+                T* act = static_cast<T*>(a.act) + static_cast<int64_t>(pair) * a.I + col0 + (c & 8) + 2 * (c & 3) + ((c >> 2) & 1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int64_t row0 = wbase + (L1 ? n * a.I + 16 * blockIdx.x : 16 * (NT * blockIdx.x + n));
-            stage<uint16_t>(reinterpret_cast<uint16_t*>(scales) + n * 16 * groups, scale_g + row0 * groups, 16 * groups);
-            if (ZEROS) stage<uint8_t>(zeros + n * 16 * groups, zero_g + row0 * groups, 16 * groups);
-            wrow[n] = codes + (row0 + (lane & 15)) * (K >> 1);
-        }
-        __syncthreads();
-        const int m = m0 + (lane & 15);
-        const T* xrow[1] = {nullptr};
-        if (m < count) {
-            const int pair = list[m];
-            xrow[0] = L1 ? static_cast<const T*>(a.x) + static_cast<int64_t>(pair / a.k) * K : static_cast<const T*>(a.act) + static_cast<int64_t>(pair) * K;
-        }
-        f32x4_t sum[1][NT] = {};
-        w4_sums<T, 1, NT, FLUSH, ZEROS, WAVES>(wrow, xrow, scales + (lane & 15) * groups, zeros + (lane & 15) * groups, K, a.gshift, sum);
-        w4_join<1, NT, WAVES>(reinterpret_cast<float*>(lds_raw), sum, [&](const float* part) {
-            constexpr int OUT = L1 ? 16 : 16 * NT;   // output columns of the workgroup
-            for (int v = threadIdx.x; v < 16 * OUT; v += 64 * WAVES) {
-                const int r = v / OUT, n = v % OUT;
-                if (m0 + r >= count) continue;
-                const int pair = list[m0 + r];
-                const float* p = part + (L1 ? 0 : (n >> 4) * 256) + w4_at(r, n & 15);
-                float s = 0.0f, u = 0.0f;
+                for (int n = 0; n < NT / 2; ++n)
+                    if (col0 + 16 * n < columns) act[16 * n] = from_f32<T>(silu_f32(v[n]) * v[n + NT / 2]);
+            } else {
+                const float w = a.topk_w[pair];
+                float* out = a.stage + static_cast<int64_t>(pair) * a.H + col0 + c;
 #pragma unroll
-                for (int w = 0; w < WAVES; ++w) {
-                    s += p[w * NT * 256];
-                    if (L1) u += p[w * NT * 256 + 256];
-                }
-                if (L1) static_cast<T*>(a.act)[static_cast<int64_t>(pair) * a.I + 16 * blockIdx.x + n] = from_f32<T>(silu_f32(s) * u);
-                else a.stage[static_cast<int64_t>(pair) * a.H + 16 * NT * blockIdx.x + n] = a.topk_w[pair] * s;
+                for (int n = 0; n < NT; ++n)
+                    if (col0 + 16 * n < columns) out[16 * n] = w * v[n];
             }
         });
     }
@@ -377,40 +471,75 @@ template <typename F> void with_group(int group, bool zeros, F&& f) {
     else z(std::integral_constant<int, 4>{});
 }
 
-constexpr int kW4Waves = 8;
+constexpr int kLdsBytes = 160 * 1024;
 
-template <typename T, int MT, int NT> hipError_t run_linear(const W4Linear& a, hipStream_t s) {
-    hipError_t err = hipSuccess;
-    with_group(1 << a.gshift, a.zeros != nullptr, [&](auto flush, auto zeros) {
-        const size_t lds = w4_lds_bytes<MT, NT, kW4Waves>(a.K >> a.gshift, zeros());
-        auto* kernel = &w4_linear_kernel<T, MT, NT, flush(), zeros(), kW4Waves>;
-        if (lds > 65536) err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
-        if (err != hipSuccess) return;
-        const dim3 grid((a.N + 16 * NT - 1) / (16 * NT), (a.M + 16 * MT - 1) / (16 * MT));
-        kernel<<<grid, 64 * kW4Waves, lds, s>>>(a);
-    });
-    return err == hipSuccess ? hipGetLastError() : err;
+// Launches `kernel` with lds bytes of dynamic LDS, which the caller has found to fit.
+template <typename K, typename A> hipError_t launch_w4(K* kernel, dim3 grid, int threads, int lds, const A& a, hipStream_t s) {
+    if (lds > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
+    kernel<<<grid, threads, lds, s>>>(a);
+    return hipGetLastError();
 }
 
-template <typename T, bool L1, int NT> hipError_t run_experts(W4Experts a, hipStream_t s) {
+template <typename T, int NT, int TEAMS, int KS> hipError_t run_linear(const W4Linear& a, hipStream_t s) {
     hipError_t err = hipSuccess;
-    const int K = L1 ? a.H : a.I, columns = L1 ? a.I : a.H;
-    const int64_t pairs = static_cast<int64_t>(a.T) * a.k;
-    with_group(1 << a.gshift, (L1 ? a.z1 : a.z2) != nullptr, [&](auto flush, auto zeros) {
-        const size_t tiles = (w4_lds_bytes<1, NT, kW4Waves>(K >> a.gshift, zeros()) + 15) / 16 * 16, lds = tiles + 4 * static_cast<size_t>(pairs);
-        a.list_at = static_cast<int>(tiles);
-        auto* kernel = &w4_experts_kernel<T, L1, NT, flush(), zeros(), kW4Waves>;
-        if (lds > 65536) err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
-        if (err != hipSuccess) return;
-        const dim3 grid(columns / (L1 ? 16 : 16 * NT), static_cast<unsigned>(pairs < a.EL ? pairs : a.EL));
-        kernel<<<grid, 64 * kW4Waves, lds, s>>>(a);
+    with_group(1 << a.gshift, a.zeros != nullptr, [&](auto flush, auto zeros) {
+        const int lds = TEAMS * w4_team_bytes<NT, KS, zeros()>(a.K >> a.gshift);
+        constexpr int columns = 16 * NT * TEAMS;
+        const int64_t grid = ((static_cast<int64_t>(a.N) + columns - 1) / columns + 7) / 8 * 8 * ((a.M + 15) / 16);
+        if (lds > kLdsBytes || grid > 0x7fffffff) {
+            err = hipErrorInvalidValue;
+            return;
+        }
+        if (a.M <= 4) err = launch_w4(&w4_linear_kernel<T, NT, flush(), zeros(), TEAMS, KS, true>, dim3(static_cast<unsigned>(grid)), 64 * TEAMS * KS, lds, a, s);
+        else err = launch_w4(&w4_linear_kernel<T, NT, flush(), zeros(), TEAMS, KS, false>, dim3(static_cast<unsigned>(grid)), 64 * TEAMS * KS, lds, a, s);
     });
-    return err == hipSuccess ? hipGetLastError() : err;
+    return err;
+}
+
+// LDS bytes of a workgroup's teams.
+template <int NT, int TEAMS, int KS> int w4_lds(int groups, bool zeros) {
+    return TEAMS * (zeros ? w4_team_bytes<NT, KS, true>(groups) : w4_team_bytes<NT, KS, false>(groups));
+}
+template <typename T, bool L1, int NT, int TEAMS, int KS> hipError_t run_experts(W4Experts a, hipStream_t s) {
+    hipError_t err = hipSuccess;
+    const int K = L1 ? a.H : a.I, columns = L1 ? a.I : a.H, pairs = a.T * a.k;
+    with_group(1 << a.gshift, (L1 ? a.z1 : a.z2) != nullptr, [&](auto flush, auto zeros) {
+        a.list_at = w4_lds<NT, TEAMS, KS>(K >> a.gshift, zeros());
+        constexpr int per = (L1 ? 8 * NT : 16 * NT) * TEAMS;
+        const int lds = a.list_at + 4 * pairs;
+        if (lds > kLdsBytes) {
+            err = hipErrorInvalidValue;
+            return;
+        }
+        err = launch_w4(&w4_experts_kernel<T, L1, NT, flush(), zeros(), TEAMS, KS>, dim3((columns + per - 1) / per, pairs < a.EL ? pairs : a.EL),
+                        64 * TEAMS * KS, lds, a, s);
+    });
+    return err;
 }
 
 template <typename T> hipError_t run_forward(const W4Experts& a, hipStream_t s) {
-    hipError_t e = run_experts<T, true, 2>(a, s);
-    if (e == hipSuccess) e = run_experts<T, false, 1>(a, s);
+    const int pairs = a.T * a.k, slots = pairs < a.EL ? pairs : a.EL;
+    // L1.  One row or so per expert: 2 + 2 tiles a workgroup (8 experts of 7168 x 4096 and back: 57 us; four
+    // tiles a wave 59 to 65 us).  More rows per expert: four tiles a wave, which then reads x half as often
+    // (128 tokens, 64 experts of 2048 x 2816 and back: 146 against 154 us), by two teams while three such
+    // workgroups fit a CU's LDS, else by one (64 tokens, 32 experts of 7168 x 4096, groups of 32: 179
+    // against 204 us).  Scales too many for those (K beyond any in use): one team of two tiles.
+    const int g1 = a.H >> a.gshift, list = 4 * pairs;
+    const bool z1 = a.z1 != nullptr, z2 = a.z2 != nullptr;
+    hipError_t e;
+    if (pairs > a.EL && w4_lds<4, 2, 2>(g1, z1) + list <= kLdsBytes / 3) e = run_experts<T, true, 4, 2, 2>(a, s);
+    else if (pairs > a.EL && w4_lds<4, 1, 4>(g1, z1) + list <= kLdsBytes / 2) e = run_experts<T, true, 4, 1, 4>(a, s);
+    else if (w4_lds<2, 2, 2>(g1, z1) + list <= kLdsBytes / 2) e = run_experts<T, true, 2, 2, 2>(a, s);
+    else e = run_experts<T, true, 2, 1, 4>(a, s);
+    if (e != hipSuccess) return e;
+    // L2.  Independent waves of two tiles, which need no joining, once there are enough of them (8 experts:
+    // 57 us against 64 us with one tile split over four waves; 6 experts of 1408 x 2048: 25 against 22 us).
+    const int g2 = a.I >> a.gshift;
+    if (static_cast<int64_t>(slots) * (a.H / 16) >= 2048 && w4_lds<2, 4, 1>(g2, z2) + list <= kLdsBytes / 2) e = run_experts<T, false, 2, 4, 1>(a, s);
+    else e = run_experts<T, false, 1, 1, 4>(a, s);
     if (e != hipSuccess) return e;
     w4_finish_kernel<T><<<dim3((a.H / 4 + 255) / 256, a.T), 256, 0, s>>>(a);
     return hipGetLastError();
@@ -418,10 +547,22 @@ template <typename T> hipError_t run_forward(const W4Experts& a, hipStream_t s) 
 
 }  // namespace
 
+// Few tiles of 16 columns: one tile a workgroup, K over as many waves as it feeds (7168 x 4096, one row: 7.2
+// us over 8 waves, 8.6 over 4; 1024 x 7168: 5.5 and 4.9 us).  More: two tiles a wave (8192 x 16384, one row:
+// 18.5 against 22.6 us), four where several row tiles share the weights or tiles abound (64 rows: 39
+// against 51 us).
+template <typename T> static hipError_t linear_rows(const W4Linear& a, hipStream_t s) {
+    const int64_t row_tiles = (a.M + 15) / 16, tiles = (static_cast<int64_t>(a.N) + 15) / 16 * row_tiles;
+    const int groups = a.K >> a.gshift;
+    if (tiles >= 1024 && (row_tiles >= 3 || tiles >= 2048) && w4_lds<4, 1, 4>(groups, a.zeros != nullptr) <= kLdsBytes / 2) return run_linear<T, 4, 1, 4>(a, s);
+    if (tiles >= 640 && w4_lds<2, 1, 4>(groups, a.zeros != nullptr) <= kLdsBytes / 2) return run_linear<T, 2, 1, 4>(a, s);
+    if (tiles > 320 || a.K < 2048) return run_linear<T, 1, 1, 4>(a, s);
+    return run_linear<T, 1, 1, 8>(a, s);
+}
+
 hipError_t launch_w4_linear(const W4Linear& a, int dtype, hipStream_t s) {
     if (a.M <= 0) return hipSuccess;
-    if (dtype == MOE_BF16) return a.M <= 16 ? run_linear<bf16_t, 1, 1>(a, s) : a.M <= 32 ? run_linear<bf16_t, 2, 1>(a, s) : run_linear<bf16_t, 4, 1>(a, s);
-    return a.M <= 16 ? run_linear<fp16_t, 1, 1>(a, s) : a.M <= 32 ? run_linear<fp16_t, 2, 1>(a, s) : run_linear<fp16_t, 4, 1>(a, s);
+    return dtype == MOE_BF16 ? linear_rows<bf16_t>(a, s) : linear_rows<fp16_t>(a, s);
 }
 
 hipError_t launch_w4_forward(const W4Experts& a, int dtype, hipStream_t s) {
