@@ -136,6 +136,49 @@ def test_ties_go_to_the_lower_id(E, n_group):
     assert idx[0].tolist() == idx[1].tolist() == list(range(8))
 
 
+@pytest.mark.parametrize("E,k", [(32, 8), (256, 8), (256, 15), (512, 6), (1000, 20), (1024, 32)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_that_differ_in_their_last_bits(E, k, sign):
+    """Runs of scores one unit in the last place apart, of every length, across the last slot too: rows of
+    pairs, rows with a run of r around slot k, whole rows of one run, rows where every fifth score is tied."""
+    g = torch.Generator().manual_seed(E + k)
+    T = 48
+    ulp = 2.0 ** -23
+    l = torch.zeros(T, E, dtype=torch.float64)
+    for t in range(T):
+        base = 1.0 - torch.arange(E, dtype=torch.float64) / (4 * E)      # 1 .. 0.75, coarse steps
+        if t % 4 == 0:
+            base[1::2] = base[0::2] - ulp
+        elif t % 4 == 1:
+            r = 2 + t % 23
+            at = max(0, k - 1 - t % 5)
+            n = min(r, E - at)
+            base[at:at + n] = base[at] - ulp * torch.arange(n, dtype=torch.float64)
+        elif t % 4 == 2:
+            base = 1.0 - ulp * torch.arange(E, dtype=torch.float64)
+        else:
+            base = 1.0 - ulp * (torch.arange(E, dtype=torch.float64) // 5)
+        l[t] = sign * base[torch.randperm(E, generator=g)]
+    l = l.float().cuda()
+    check(l, k)
+    check(l, k, bias=torch.zeros(E).cuda(), n_group=4, topk_group=3, score="sigmoid")
+    check(l.bfloat16(), k, bias=(ulp * torch.randint(0, 4, (E,), generator=g)).float().cuda())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_best_all_in_one_lane(dtype):
+    """Scores laid out so that one lane holds many of the row's best, whatever it keeps of them."""
+    for E in (128, 256, 384, 512, 1024):
+        l = logits_of(40, E, dtype, E)
+        n = 4 if dtype == torch.float32 else 8
+        for t in range(40):
+            lane = t % 16
+            ids = [e for e in range(E) if e // n % 16 == lane][: 2 + t % 14]
+            l[t, ids] = (10 + torch.randperm(len(ids), generator=torch.Generator().manual_seed(t))).to(dtype).cuda()
+        for k in (3, 8, 15, 24):
+            check(l, k)
+
+
 @pytest.mark.parametrize("score,renormalize", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
 @pytest.mark.parametrize("E,n_group,topk_group", [(16, 1, 1), (64, 4, 2), (520, 1, 1)])
 def test_rows_with_few_or_no_experts_and_extreme_logits(E, n_group, topk_group, score, renormalize):

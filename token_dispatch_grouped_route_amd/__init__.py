@@ -468,15 +468,15 @@ def _place(t, name, stream):
         if stream.device != t.device:
             raise MoeError("stream is on %s, %s on %s" % (stream.device, name, t.device))
         return torch.cuda.stream(stream)
-    return _HERE_ALREADY if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    return _HERE_ALREADY if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
-def _like(t, dtype, name, shape, like):
-    """Address of a contiguous tensor of this dtype and shape on like's device (None stays None)."""
+def _like(t, dtype, name, shape, dev):
+    """Address of a contiguous tensor of this dtype and shape on GPU dev (None stays None)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != like.device or not t.is_contiguous():
-        raise MoeError("%s must be a contiguous %s tensor on %s" % (name, dtype, like.device))
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise MoeError("%s must be a contiguous %s tensor on GPU %d" % (name, dtype, dev))
     if t.shape != shape:
         raise MoeError("%s has the shape %s; %s is needed" % (name, tuple(t.shape), tuple(shape)))
     return t.data_ptr()
@@ -512,38 +512,39 @@ def _rows(t, name, like=None, shape=None):
     """(address, leading dimension, rows, columns) of a tensor seen as rows of its last dimension."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() < 1:
         raise MoeError("%s must be a tensor of rows on a GPU" % name)
-    if like is not None and (t.device != like.device or t.dtype != like.dtype or t.shape != shape):
+    if like is not None and (t.get_device() != like.get_device() or t.dtype != like.dtype or t.shape != shape):
         raise MoeError("%s must be %s of the shape %s on %s" % (name, like.dtype, tuple(shape), like.device))
     cols = t.shape[-1]
     if cols == 0:
         raise MoeError("%s has rows of no element" % name)
-    ld = _row_stride(t)
+    ld = cols if t.is_contiguous() else _row_stride(t)
     if ld is None:
         raise MoeError("%s must have contiguous rows, evenly spaced, that do not overlap" % name)
     return t.data_ptr(), ld, t.numel() // cols, cols
 
 
-def _handle():
-    """The current stream of the current device (without the Stream object, which takes 3 us to make)."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+def _handle(dev):
+    """The current stream of GPU dev (without the Stream object, which takes 3 us to make)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def norm_forward(x, weight=None, bias=None, eps=1e-5, kind="layer", y=None, stream=None):
     """(y, mean, rstd) of the row norm of x over its last dimension (moe_norm_forward): kind "layer" or
     "rms" (no bias; mean is None).  weight and bias in x's dtype or fp32.  mean and rstd fp32, one per row."""
     with _place(x, "x", stream):
+        dev = x.get_device()
         px, ldx, rows, cols = _rows(x, "x")
         wd = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            y = torch.empty_like(x, memory_format=torch.contiguous_format)
             py, ldy = y.data_ptr(), cols
         else:
             py, ldy = _rows(y, "y", x, x.shape)[:2]
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if kind == "layer" else None
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         _check(lib().moe_norm_forward(_code(_KIND, kind, "kind"), _code(_DTYPE, x.dtype, "x.dtype"), _code(_DTYPE, wd, "weight.dtype"), rows, cols,
-                                      px, ldx, _like(weight, wd, "weight", (cols,), x), _like(bias, wd, "bias", (cols,), x), eps, py, ldy,
-                                      mean.data_ptr() if mean is not None else None, rstd.data_ptr(), _handle()), "moe_norm_forward")
+                                      px, ldx, _like(weight, wd, "weight", (cols,), dev), _like(bias, wd, "bias", (cols,), dev), eps, py, ldy,
+                                      mean.data_ptr() if mean is not None else None, rstd.data_ptr(), _handle(dev)), "moe_norm_forward")
     return y, mean, rstd
 
 
@@ -551,11 +552,12 @@ def norm_backward(dy, x, weight, mean, rstd, kind="layer", bias=False, dx=True, 
     """(dx, dweight, dbias) of norm_forward (moe_norm_backward); dweight is None without a weight, dbias
     without bias (a truth value: whether its gradient is wanted), dx with dx=False."""
     with _place(x, "x", stream):
+        dev = x.get_device()
         px, ldx, rows, cols = _rows(x, "x")
         pdy, lddy = _rows(dy, "dy", x, x.shape)[:2]
         dt = _code(_DTYPE, x.dtype, "x.dtype")
         wd = weight.dtype if weight is not None else x.dtype
-        gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx else None
+        gx = torch.empty_like(x, memory_format=torch.contiguous_format) if dx else None
         gw = torch.empty(cols, dtype=wd, device=x.device) if weight is not None else None
         gb = torch.empty(cols, dtype=wd, device=x.device) if bias else None
         if gx is None and gw is None and gb is None:
@@ -565,8 +567,8 @@ def norm_backward(dy, x, weight, mean, rstd, kind="layer", bias=False, dx=True, 
         p = lambda t: t.data_ptr() if t is not None else None
         stats = x.shape[:-1]
         _check(lib().moe_norm_backward(_code(_KIND, kind, "kind"), dt, _code(_DTYPE, wd, "weight.dtype"), rows, cols, pdy, lddy, px, ldx,
-                                       _like(weight, wd, "weight", (cols,), x), _like(mean, torch.float32, "mean", stats, x),
-                                       _like(rstd, torch.float32, "rstd", stats, x), p(gx), cols, p(gw), p(gb), p(ws), nbytes, _handle()),
+                                       _like(weight, wd, "weight", (cols,), dev), _like(mean, torch.float32, "mean", stats, dev),
+                                       _like(rstd, torch.float32, "rstd", stats, dev), p(gx), cols, p(gw), p(gb), p(ws), nbytes, _handle(dev)),
                "moe_norm_backward")
     return gx, gw, gb
 
@@ -614,6 +616,7 @@ def route_topk(logits, k, bias=None, score="softmax", renormalize=True, n_group=
     """(topk_idx int32 [T, k], topk_w fp32 [T, k]) of router logits [T, E] (moe_route_topk): what moe_layer
     and the forward entry points take as their routing.  `router` is the differentiable form."""
     with _place(logits, "logits", stream):
+        dev = logits.get_device()
         if logits.dim() != 2:
             raise MoeError("logits must be [T, E]")
         p, ld, T, E = _rows(logits, "logits")
@@ -621,16 +624,17 @@ def route_topk(logits, k, bias=None, score="softmax", renormalize=True, n_group=
             topk_idx = torch.empty(T, k, dtype=torch.int32, device=logits.device)
         if topk_w is None:
             topk_w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
-        _check(lib().moe_route_topk(_code(_DTYPE, logits.dtype, "logits.dtype"), T, E, k, p, ld, _like(bias, torch.float32, "bias", (E,), logits),
+        _check(lib().moe_route_topk(_code(_DTYPE, logits.dtype, "logits.dtype"), T, E, k, p, ld, _like(bias, torch.float32, "bias", (E,), dev),
                                     _code(_SCORE, score, "score"), bool(renormalize), n_group, topk_group, scale,
-                                    _like(topk_idx, torch.int32, "topk_idx", (T, k), logits), _like(topk_w, torch.float32, "topk_w", (T, k), logits),
-                                    _handle()), "moe_route_topk")
+                                    _like(topk_idx, torch.int32, "topk_idx", (T, k), dev), _like(topk_w, torch.float32, "topk_w", (T, k), dev),
+                                    _handle(dev)), "moe_route_topk")
     return topk_idx, topk_w
 
 
 def route_topk_backward(logits, topk_idx, dtopk_w, score="softmax", renormalize=True, scale=1.0, dlogits=None, stream=None):
     """dlogits [T, E] of route_topk for the gradient dtopk_w [T, k] (moe_route_topk_backward)."""
     with _place(logits, "logits", stream):
+        dev = logits.get_device()
         if logits.dim() != 2 or topk_idx.dim() != 2:
             raise MoeError("logits must be [T, E] and topk_idx [T, k]")
         p, ld, T, E = _rows(logits, "logits")
@@ -638,9 +642,9 @@ def route_topk_backward(logits, topk_idx, dtopk_w, score="softmax", renormalize=
         if dlogits is None:
             dlogits = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
         pd, ldd = _rows(dlogits, "dlogits", logits, logits.shape)[:2]
-        _check(lib().moe_route_topk_backward(_code(_DTYPE, logits.dtype, "logits.dtype"), T, E, k, p, ld, _like(topk_idx, torch.int32, "topk_idx", (T, k), logits),
-                                             _like(dtopk_w, torch.float32, "dtopk_w", (T, k), logits), _code(_SCORE, score, "score"),
-                                             bool(renormalize), scale, pd, ldd, _handle()), "moe_route_topk_backward")
+        _check(lib().moe_route_topk_backward(_code(_DTYPE, logits.dtype, "logits.dtype"), T, E, k, p, ld, _like(topk_idx, torch.int32, "topk_idx", (T, k), dev),
+                                             _like(dtopk_w, torch.float32, "dtopk_w", (T, k), dev), _code(_SCORE, score, "score"),
+                                             bool(renormalize), scale, pd, ldd, _handle(dev)), "moe_route_topk_backward")
     return dlogits
 
 
@@ -673,6 +677,7 @@ def w4_quantize(w, group=128, zeros=False, dtype=None, stream=None):
     uint8 [E, N, K / 2], dtype [E, N, K / group] and uint8 [E, N, K / group].  dtype, that of the
     activations to come, is w's own, or bf16 for fp32 weights."""
     with _place(w, "w", stream):
+        dev = w.get_device()
         if w.dim() not in (2, 3) or not w.is_contiguous():
             raise MoeError("w must be contiguous, [E, K, N] or [K, N]")
         if dtype is None:
@@ -684,24 +689,26 @@ def w4_quantize(w, group=128, zeros=False, dtype=None, stream=None):
         scales = torch.empty(lead + (N, K // group), dtype=dtype, device=w.device)
         points = torch.empty(lead + (N, K // group), dtype=torch.uint8, device=w.device) if zeros else None
         _check(lib().moe_w4_quantize(_code(_DTYPE, w.dtype, "w.dtype"), _code(_DTYPE, dtype, "dtype"), lead[0] if lead else 1, K, N, group, w.data_ptr(),
-                                     codes.data_ptr(), scales.data_ptr(), points.data_ptr() if zeros else None, _handle()), "moe_w4_quantize")
+                                     codes.data_ptr(), scales.data_ptr(), points.data_ptr() if zeros else None, _handle(dev)), "moe_w4_quantize")
     return codes, scales, points
 
 
 def _w4(w, name, x, lead, N, K):
     """Addresses of a (codes, scales, zeros) triple of N columns and reduction length K, and its group."""
     codes, scales, zeros = w
+    dev = x.get_device()
     if not isinstance(scales, torch.Tensor) or scales.dim() != len(lead) + 2 or scales.shape[-1] < 1 or K % scales.shape[-1] != 0:
         raise MoeError("%s: scales must be [%sN, K / group]" % (name, "E, " * len(lead)))
     groups = scales.shape[-1]
-    return (_like(codes, torch.uint8, name + " codes", lead + (N, K // 2), x), _like(scales, x.dtype, name + " scales", lead + (N, groups), x),
-            _like(zeros, torch.uint8, name + " zeros", lead + (N, groups), x), K // groups)
+    return (_like(codes, torch.uint8, name + " codes", lead + (N, K // 2), dev), _like(scales, x.dtype, name + " scales", lead + (N, groups), dev),
+            _like(zeros, torch.uint8, name + " zeros", lead + (N, groups), dev), K // groups)
 
 
 def w4_linear(x, codes, scales, zeros=None, y=None, stream=None):
     """y [..., N] = x [..., K] times the 4-bit weights (codes uint8 [N, K / 2], scales [N, K / group] in x's
     dtype, zeros uint8 [N, K / group] or None), for few rows (moe_w4_linear)."""
     with _place(x, "x", stream):
+        dev = x.get_device()
         px, ldx, M, K = _rows(x, "x")
         if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
             raise MoeError("codes must be [N, K / 2]")
@@ -713,7 +720,7 @@ def w4_linear(x, codes, scales, zeros=None, y=None, stream=None):
             py, ldy = y.data_ptr(), N
         else:
             py, ldy = _rows(y, "y", x, shape)[:2]
-        _check(lib().moe_w4_linear(_code(_DTYPE, x.dtype, "x.dtype"), M, N, K, group, px, ldx, pc, ps, pz, py, ldy, _handle()), "moe_w4_linear")
+        _check(lib().moe_w4_linear(_code(_DTYPE, x.dtype, "x.dtype"), M, N, K, group, px, ldx, pc, ps, pz, py, ldy, _handle(dev)), "moe_w4_linear")
     return y
 
 
@@ -733,8 +740,9 @@ def forward_w4(shape, x, topk_idx, topk_w, w1, w2, ws, y=None, stream=None):
     bf16 or fp16 [T, H]; w1 and w2 are (codes, scales, zeros or None) of w4_quantize for W1 [EL, H, 2I] and
     W2 [EL, I, H], with one group size; ws is w4_alloc_workspace(shape)'s."""
     with _place(x, "x", stream):
+        dev = x.get_device()
         T, H, I, EL = shape.T, shape.H, shape.I, shape.EL
-        px = _like(x, x.dtype, "x", (T, H), x)
+        px = _like(x, x.dtype, "x", (T, H), dev)
         one, two = _w4(w1, "w1", x, (EL,), 2 * I, H), _w4(w2, "w2", x, (EL,), H, I)
         if one[3] != two[3]:
             raise MoeError("w1 and w2 have groups of %d and %d" % (one[3], two[3]))
@@ -744,6 +752,6 @@ def forward_w4(shape, x, topk_idx, topk_w, w1, w2, ws, y=None, stream=None):
         if ws.device != x.device:
             raise MoeError("ws is on %s, x on %s" % (ws.device, x.device))
         _check(lib().moe_forward_w4(ctypes.byref(shape), _code(_DTYPE, x.dtype, "x.dtype"), one[3], px,
-                                    _like(topk_idx, torch.int32, "topk_idx", (T, shape.k), x), _like(topk_w, torch.float32, "topk_w", (T, shape.k), x),
-                                    *one[:3], *two[:3], p, n, _like(y, x.dtype, "y", (T, H), x), _handle()), "moe_forward_w4")
+                                    _like(topk_idx, torch.int32, "topk_idx", (T, shape.k), dev), _like(topk_w, torch.float32, "topk_w", (T, shape.k), dev),
+                                    *one[:3], *two[:3], p, n, _like(y, x.dtype, "y", (T, H), dev), _handle(dev)), "moe_forward_w4")
     return y

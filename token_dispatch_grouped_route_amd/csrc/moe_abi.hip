@@ -579,6 +579,10 @@ int32_t moe_route_topk(int32_t dtype, int32_t T, int32_t E, int32_t k, const voi
     if (!is_gfx950()) return MOE_ERR_DEVICE;
     RouteArgs a = {};
     a.T = T, a.E = E, a.k = k, a.n_group = n_group, a.topk_group = topk_group, a.sigmoid = score == MOE_SIGMOID;
+    const int per_chunk = 16 / elem_bytes(dtype), chunks = E / n_group / per_chunk;
+    a.group_shift = E / n_group % per_chunk == 0 && chunks <= 16 && (chunks & (chunks - 1)) == 0 ? __builtin_ctz(static_cast<unsigned>(chunks)) : -1;
+    a.id_mask = 1;
+    while (a.id_mask + 1 < static_cast<uint32_t>(E)) a.id_mask = 2 * a.id_mask + 1;
     a.renorm = renormalize != 0, a.scale = scale, a.logits = logits, a.ld = ld, a.bias = bias, a.idx_out = topk_idx, a.w_out = topk_w;
     return launched(launch_route_topk(a, dtype, false, static_cast<hipStream_t>(stream)));
 }

@@ -194,6 +194,8 @@ hipError_t launch_norm_bwd(const NormArgs& a, int dtype, int wdtype, bool layer,
 // Top-k router (moe_route_topk / moe_route_topk_backward).
 struct RouteArgs {
     int32_t T, E, k, n_group, topk_group;
+    uint32_t id_mask;      // the smallest 2^b - 1 that holds every id
+    int32_t group_shift;   // log2 of a group's 16-byte chunks of logits, if those are 1, 2, 4, 8 or 16; else -1
     bool sigmoid, renorm;
     float scale;
     const void* logits;
