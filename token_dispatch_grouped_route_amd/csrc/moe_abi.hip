@@ -508,7 +508,8 @@ bool bad_ld(int64_t ld, int64_t rows, int64_t cols) { return ld < cols || (rows 
 
 size_t moe_norm_workspace_bytes(int32_t dtype, int64_t rows, int32_t cols) {
     if (check_norm(MOE_LAYER_NORM, dtype, dtype, rows, cols) != MOE_OK) return 0;
-    const size_t part = align_up(static_cast<size_t>(norm_bwd_slots(rows, cols, elem_bytes(dtype))) * cols * 4);
+    const int64_t rms = norm_bwd_slots(rows, cols, elem_bytes(dtype), false), layer = norm_bwd_slots(rows, cols, elem_bytes(dtype), true);
+    const size_t part = align_up(static_cast<size_t>(rms > layer ? rms : layer) * cols * 4);
     return 2 * (part > 0 ? part : kWsAlign);
 }
 

@@ -187,7 +187,7 @@ struct NormArgs {
     float *mean, *rstd;
     float *part_w, *part_b;   // [slots, cols] partial rows of dweight and dbias
 };
-int64_t norm_bwd_slots(int64_t rows, int cols, int elem_bytes);
+int64_t norm_bwd_slots(int64_t rows, int cols, int elem_bytes, bool layer);
 hipError_t launch_norm_fwd(const NormArgs& a, int dtype, int wdtype, bool layer, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, int dtype, int wdtype, bool layer, hipStream_t s);
 

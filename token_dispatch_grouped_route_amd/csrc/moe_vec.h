@@ -38,6 +38,32 @@ template <typename T> __device__ __forceinline__ u32x4_t load_chunk(const T* p, 
     return __builtin_bit_cast(u32x4_t, c);
 }
 
+// The same in two steps for kernels that load ahead: load_ahead() is one unconditional load (the last 16
+// bytes of the row for a chunk that reaches past its end), settle() shifts what it brought into place, under
+// a branch that only the last chunks' waves take.  Branches around the loads themselves kept them from being
+// issued together and cost registers at every merge.  Rows shorter than a chunk (SHORT) are read by element.
+template <typename T, bool SHORT> __device__ __forceinline__ u32x4_t load_ahead(const T* row, int c, int cols) {
+    constexpr int N = Chunk<T>::N;
+    if (SHORT && cols < N) return load_chunk<T>(row, c == 0 ? cols : 0);
+    return *reinterpret_cast<const u32x4_any_t*>(row + min(c, cols - N));
+}
+template <typename T, bool SHORT> __device__ __forceinline__ u32x4_t settle(u32x4_t v, int c, int cols) {
+    constexpr int N = Chunk<T>::N;
+    if ((SHORT && cols < N) || c <= cols - N) return v;
+    const int past = c - (cols - N);   // elements to drop at the front: the chunk begins there
+    if (past >= N) return u32x4_t{0, 0, 0, 0};
+    const int bytes = past * static_cast<int>(sizeof(T));
+    if (bytes & 8) v = u32x4_t{v[2], v[3], 0, 0};
+    if (bytes & 4) v = u32x4_t{v[1], v[2], v[3], 0};
+    if (bytes & 2) {
+        v[0] = __builtin_amdgcn_alignbyte(v[1], v[0], 2);
+        v[1] = __builtin_amdgcn_alignbyte(v[2], v[1], 2);
+        v[2] = __builtin_amdgcn_alignbyte(v[3], v[2], 2);
+        v[3] >>= 16;
+    }
+    return v;
+}
+
 template <typename T> __device__ __forceinline__ void store_chunk(T* p, u32x4_t raw, int valid) {
     constexpr int N = Chunk<T>::N;
     if (valid >= N) {
