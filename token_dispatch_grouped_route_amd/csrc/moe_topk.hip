@@ -434,9 +434,9 @@ __global__ __launch_bounds__(256) void route_topk_bwd_kernel(RouteArgs a) {
     const float q = a.renorm || DENSE ? row_sum<LPR>(p * g) : 0.0f;
     float d = a.renorm ? p * (g - q) : p * g;
     if (a.sigmoid) d *= sigmoid_f32(-l);   // 1 - sigmoid(l)
-    __builtin_amdgcn_wave_barrier();       // a row's LDS is its wave's alone, and a wave's accesses stay in order
+    wave_sync();   // a row's LDS is its wave's alone
     if (there) atomicAdd(mine + pick, d);
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     const float share = DENSE && all_sum > 0.0f ? q / all_sum : 0.0f;
     T* dx = static_cast<T*>(a.dlogits) + r * a.ldd;
 #pragma unroll

@@ -228,10 +228,10 @@ template <int NT, int KS, bool ZEROS> __host__ __device__ inline int w4_team_byt
     return ((meta > sums ? meta : sums) + 15) / 16 * 16;
 }
 
-// Orders a team's LDS accesses: nothing to wait for in a wave of its own.
+// Orders a team's LDS accesses.
 template <int KS> __device__ __forceinline__ void team_barrier() {
     if constexpr (KS > 1) lds_barrier();
-    else __builtin_amdgcn_wave_barrier();
+    else wave_sync();
 }
 
 // f(m, col, values) for the elements of a team's tiles: row m, column col of each tile (values[n]).  The
@@ -333,7 +333,7 @@ __device__ __forceinline__ int w4_pairs(const W4Experts& a, int id, int first, i
         if (m != 0 && count == 0) earliest = p0 + __ffsll(static_cast<unsigned long long>(m)) - 1;
         count += __popcll(m);
     }
-    __builtin_amdgcn_wave_barrier();   // the list is read by other lanes than those that wrote it
+    wave_sync();   // the list is read by other lanes than those that wrote it
     return earliest < first ? 0 : count;
 }
 
