@@ -387,7 +387,7 @@ size_t moe_norm_workspace_bytes(int32_t dtype, int64_t rows, int32_t cols);
  * summed in fp32 in an order that the sizes fix.  dx, dweight and dbias may each be NULL, not all; dbias
  * is for layer norm only (MOE_ERR_SHAPE).  rows == 0 writes zeros to dweight and dbias.  mean (layer
  * norm) and rstd as the forward wrote them.  ws [device], moe_norm_workspace_bytes bytes, 256-B
- * aligned, is scratch; it may be NULL when neither dweight nor dbias is asked for.  dx must not overlap
+ * aligned, is scratch that no other call in flight may share; it may be NULL when neither dweight nor dbias is asked for.  dx must not overlap
  * x or dy.
  */
 int32_t moe_norm_backward(int32_t kind, int32_t dtype, int32_t wdtype, int64_t rows, int32_t cols, const void* dy, int64_t lddy,
@@ -407,7 +407,7 @@ int32_t moe_norm_backward(int32_t kind, int32_t dtype, int32_t wdtype, int64_t r
  *   topk_w [device] fp32 [T, k]: scale * p, 0 in those slots, with p = exp(l) (MOE_SOFTMAX) divided by
  *   its sum over the chosen experts (renormalize != 0) or over all in service, or p = 1 / (1 + exp(-l))
  *   (MOE_SIGMOID), divided by its sum over the chosen (renormalize != 0) or not.
- * T >= 0, E 1 .. 1024, k 1 .. min(32, E), n_group 1 .. 16 a divisor of E, topk_group 1 .. n_group.
+ * T 0 .. 2^25, E 1 .. 1024, k 1 .. min(32, E), n_group 1 .. 16 a divisor of E, topk_group 1 .. n_group.
  */
 int32_t moe_route_topk(int32_t dtype, int32_t T, int32_t E, int32_t k, const void* logits, int64_t ld, const float* bias,
                        int32_t score, int32_t renormalize, int32_t n_group, int32_t topk_group, float scale,
@@ -435,16 +435,18 @@ int32_t moe_route_topk_backward(int32_t dtype, int32_t T, int32_t E, int32_t k, 
  * moe_w4_quantize makes them from w [device] wdtype [E, K, N] (the logical x @ W layout): zeros NULL:
  * scale = max |w| / 7; else scale = (max(w, 0) - min(w, 0)) / 15 and zero = -min(w, 0) / scale rounded;
  * the scale is rounded to dtype, the code is the nearest integer to w / scale + zero (ties to even)
- * kept in 0 .. 15.  A group of zeros has scale 0.  The weights have to be finite.
+ * kept in 0 .. 15.  A group of zeros has scale 0.  The weights have to be finite, and their scales within dtype.
+ * N and K as for moe_w4_linear; E 1 .. 65535.
  */
 int32_t moe_w4_quantize(int32_t wdtype, int32_t dtype, int32_t E, int32_t K, int32_t N, int32_t group, const void* w,
                         uint8_t* codes, void* scales, uint8_t* zeros, void* stream);
 
 /*
- * y[m, n] = sum over k of x[m, k] * weight(n, k), for few rows (each 64 rows stream the weights once):
+ * y[m, n] = sum over k of x[m, k] * weight(n, k), for few rows (each 16 rows read the weights once):
  * x [device] dtype [M, K] (leading dimension ldx, a multiple of 8 up to 2^23; 16-byte aligned), y [device] dtype
  * [M, N] (ldy).  The codes are multiplied unscaled and summed in fp32; each group's scale enters in fp32.
- * M 0 .. 1048576, N >= 1, K a multiple of group.  A non-finite activation makes its row of y non-finite.
+ * M 0 .. 1048576, N 1 .. 2^28, at most 2^23 tiles of 16 x 16 elements of y, K a multiple of group.  y must not
+ * overlap x.  A non-finite activation makes its row of y non-finite.
  */
 int32_t moe_w4_linear(int32_t dtype, int32_t M, int32_t N, int32_t K, int32_t group, const void* x, int64_t ldx,
                       const uint8_t* codes, const void* scales, const uint8_t* zeros, void* y, int64_t ldy, void* stream);
@@ -460,7 +462,8 @@ size_t moe_w4_workspace_bytes(const moe_shape* shape);
  * SwiGLU is applied in fp32 and the activation rounded to dtype; L2 sums, weights and combines in fp32
  * in slot order (the same bits on every run); y [device] dtype [T, H].  An expert's weights are read
  * once per 16 of its pairs.  T * k at most 4096 (MOE_ERR_SHAPE): longer batches are for moe_forward and
- * moe_forward_mx.  shape->train must be 0; block_m is not used.  ws [device] 256-B aligned scratch.
+ * moe_forward_mx.  shape->train must be 0; block_m is not used.  ws [device] 256-B aligned scratch, which calls
+ * in flight at the same time (and graphs replayed at the same time) must not share.
  */
 int32_t moe_forward_w4(const moe_shape* shape, int32_t dtype, int32_t group, const void* x, const int32_t* topk_idx,
                        const float* topk_w, const uint8_t* w1, const void* s1, const uint8_t* z1, const uint8_t* w2,

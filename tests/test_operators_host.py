@@ -64,7 +64,7 @@ def route_bwd(dtype=2, T=4, E=64, k=8, logits=A, ld=64, idx=B, dw=B, score=0, re
 
 
 @pytest.mark.parametrize("bad,status", [
-    (dict(dtype=3), SHAPE), (dict(T=-1), SHAPE), (dict(E=0), SHAPE), (dict(E=1025, ld=1025), SHAPE), (dict(k=0), SHAPE), (dict(k=33), SHAPE),
+    (dict(dtype=3), SHAPE), (dict(T=-1), SHAPE), (dict(T=(1 << 25) + 1), SHAPE), (dict(E=0), SHAPE), (dict(E=1025, ld=1025), SHAPE), (dict(k=0), SHAPE), (dict(k=33), SHAPE),
     (dict(E=4, k=5), SHAPE), (dict(ld=63), SHAPE), (dict(score=2), SHAPE), (dict(n_group=0), SHAPE), (dict(n_group=17), SHAPE), (dict(n_group=3), SHAPE),
     (dict(n_group=4, topk_group=5), SHAPE), (dict(n_group=4, topk_group=0), SHAPE), (dict(logits=None), NULL), (dict(idx=None), NULL), (dict(w=None), NULL),
     (dict(logits=A + 2), ALIGN), (dict(bias=B + 2), ALIGN), (dict(idx=C + 1), ALIGN),
@@ -74,7 +74,7 @@ def test_route_refusals(bad, status):
 
 
 @pytest.mark.parametrize("bad,status", [
-    (dict(k=33), SHAPE), (dict(ldd=63), SHAPE), (dict(score=-1), SHAPE), (dict(idx=None), NULL), (dict(dw=None), NULL), (dict(out=None), NULL),
+    (dict(k=33), SHAPE), (dict(T=(1 << 25) + 1), SHAPE), (dict(ldd=63), SHAPE), (dict(score=-1), SHAPE), (dict(idx=None), NULL), (dict(dw=None), NULL), (dict(out=None), NULL),
     (dict(out=A), SHAPE), (dict(out=C + 2), ALIGN),
 ])
 def test_route_backward_refusals(bad, status):
@@ -96,14 +96,14 @@ def linear(dtype=0, M=2, N=64, K=256, group=64, x=A, ldx=256, codes=B, scales=C,
 
 @pytest.mark.parametrize("bad,status", [
     (dict(wdtype=3), SHAPE), (dict(dtype=2), SHAPE), (dict(E=0), SHAPE), (dict(group=16), SHAPE), (dict(group=96, K=288), SHAPE), (dict(K=200), SHAPE),
-    (dict(K=65536), SHAPE), (dict(N=0), SHAPE), (dict(w=None), NULL), (dict(codes=None), NULL), (dict(scales=None), NULL), (dict(codes=B + 8), ALIGN), (dict(zeros=B + 4), ALIGN),
+    (dict(K=65536), SHAPE), (dict(N=0), SHAPE), (dict(N=(1 << 28) + 1), SHAPE), (dict(w=None), NULL), (dict(codes=None), NULL), (dict(scales=None), NULL), (dict(codes=B + 8), ALIGN), (dict(zeros=B + 4), ALIGN),
 ])
 def test_quantize_refusals(bad, status):
     assert quantize(**bad) == status
 
 
 @pytest.mark.parametrize("bad,status", [
-    (dict(dtype=2), SHAPE), (dict(M=-1), SHAPE), (dict(M=(1 << 20) + 1), SHAPE), (dict(N=0), SHAPE), (dict(group=48), SHAPE), (dict(K=0), SHAPE), (dict(ldx=255), SHAPE),
+    (dict(dtype=2), SHAPE), (dict(M=-1), SHAPE), (dict(M=(1 << 20) + 1), SHAPE), (dict(M=1 << 20, N=2049, ldy=2049), SHAPE), (dict(N=0), SHAPE), (dict(group=48), SHAPE), (dict(K=0), SHAPE), (dict(ldx=255), SHAPE),
     (dict(ldy=63), SHAPE), (dict(x=None), NULL), (dict(codes=None), NULL), (dict(y=None), NULL), (dict(x=A + 8), ALIGN), (dict(ldx=260), ALIGN),
     (dict(scales=C + 2), ALIGN), (dict(y=C + 1), ALIGN),
 ])

@@ -491,7 +491,9 @@ int32_t moe_forward_mx(const moe_shape* shape, const uint8_t* xq, const uint8_t*
 // ---------------------------------------------------------------------------------------------
 namespace {
 constexpr int kNormMaxCols = 32768, kW4MaxK = 32768;
-constexpr int64_t kW4MaxLd = 1 << 23;   // 64 rows of x stay within 32-bit byte offsets
+constexpr int64_t kW4MaxLd = 1 << 23;   // 16 rows of x stay within 32-bit byte offsets
+constexpr int kRouteMaxT = 1 << 25;        // a grid has fewer than 2^32 threads: 64 per token,
+constexpr int64_t kW4MaxTiles = 1 << 23;   // and 256 per 16 x 16 tile of moe_w4_linear's y
 bool is_dtype(int32_t t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
 bool is_16bit(int32_t t) { return t == MOE_BF16 || t == MOE_FP16; }
 int elem_bytes(int32_t t) { return t == MOE_FP32 ? 4 : 2; }
@@ -563,7 +565,7 @@ int32_t moe_norm_backward(int32_t kind, int32_t dtype, int32_t wdtype, int64_t r
 
 namespace {
 int32_t check_route(int32_t dtype, int32_t T, int32_t E, int32_t k, int64_t ld, int32_t score) {
-    if (!is_dtype(dtype) || T < 0 || E < 1 || E > 1024 || k < 1 || k > 32 || k > E || bad_ld(ld, T, E)) return MOE_ERR_SHAPE;
+    if (!is_dtype(dtype) || T < 0 || T > kRouteMaxT || E < 1 || E > 1024 || k < 1 || k > 32 || k > E || bad_ld(ld, T, E)) return MOE_ERR_SHAPE;
     return score == MOE_SOFTMAX || score == MOE_SIGMOID ? MOE_OK : MOE_ERR_SHAPE;
 }
 }  // namespace
@@ -623,7 +625,7 @@ bool w4_layout(const moe_shape* s, size_t* stage, size_t* total) {
 
 int32_t moe_w4_quantize(int32_t wdtype, int32_t dtype, int32_t E, int32_t K, int32_t N, int32_t group, const void* w,
                         uint8_t* codes, void* scales, uint8_t* zeros, void* stream) {
-    if (!is_dtype(wdtype) || !is_16bit(dtype) || E < 1 || E > 65535 || N < 1 || group_shift(group, K) < 0) return MOE_ERR_SHAPE;
+    if (!is_dtype(wdtype) || !is_16bit(dtype) || E < 1 || E > 65535 || N < 1 || N > (1 << 28) || group_shift(group, K) < 0) return MOE_ERR_SHAPE;
     if (!w || !codes || !scales) return MOE_ERR_NULL;
     if (!aligned_to(w, wdtype) || !aligned16(codes) || !aligned16(scales) || !aligned16(zeros)) return MOE_ERR_ALIGN;
     if (!is_gfx950()) return MOE_ERR_DEVICE;
@@ -634,7 +636,7 @@ int32_t moe_w4_linear(int32_t dtype, int32_t M, int32_t N, int32_t K, int32_t gr
                       const uint8_t* codes, const void* scales, const uint8_t* zeros, void* y, int64_t ldy, void* stream) {
     const int gshift = group_shift(group, K);
     if (!is_16bit(dtype) || M < 0 || M > (1 << 20) || N < 1 || N > (1 << 28) || gshift < 0 || bad_ld(ldx, M, K) || bad_ld(ldy, M, N)) return MOE_ERR_SHAPE;
-    if (ldx > kW4MaxLd) return MOE_ERR_SHAPE;
+    if (ldx > kW4MaxLd || (static_cast<int64_t>(M) + 15) / 16 * ((static_cast<int64_t>(N) + 15) / 16) > kW4MaxTiles) return MOE_ERR_SHAPE;
     if (M == 0) return MOE_OK;
     if (!x || !codes || !scales || !y) return MOE_ERR_NULL;
     if (!aligned16(x) || ldx % 8 != 0 || !aligned16(codes) || !aligned16(scales) || !aligned16(zeros) || !aligned_to(y, dtype)) return MOE_ERR_ALIGN;

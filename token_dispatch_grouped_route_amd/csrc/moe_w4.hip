@@ -489,7 +489,7 @@ template <typename T, int NT, int TEAMS, int KS> hipError_t run_linear(const W4L
         const int lds = TEAMS * w4_team_bytes<NT, KS, zeros()>(a.K >> a.gshift);
         constexpr int columns = 16 * NT * TEAMS;
         const int64_t grid = ((static_cast<int64_t>(a.N) + columns - 1) / columns + 7) / 8 * 8 * ((a.M + 15) / 16);
-        if (lds > kLdsBytes || grid > 0x7fffffff) {
+        if (lds > kLdsBytes) {
             err = hipErrorInvalidValue;
             return;
         }
