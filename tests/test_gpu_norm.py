@@ -254,6 +254,8 @@ def test_autograd_forms():
     w2 = torch.ones(96, device="cuda", requires_grad=True)
     moe.layer_norm(x, w2).sum().backward()     # x frozen
     assert torch.equal(w.grad, w2.grad)
+    gx, gw, gb = moe.norm_backward(x, x, w2.detach(), *moe.norm_forward(x, w2.detach())[1:], bias=True, dweight=False)
+    assert gw is None and gx is not None and gb.dtype == torch.float32
     bias = torch.zeros(96, dtype=torch.bfloat16, device="cuda", requires_grad=True)
     moe.layer_norm(x, None, bias).sum().backward()
     assert (bias.grad == 20).all()

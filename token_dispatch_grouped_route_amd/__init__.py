@@ -548,9 +548,9 @@ def norm_forward(x, weight=None, bias=None, eps=1e-5, kind="layer", y=None, stre
     return y, mean, rstd
 
 
-def norm_backward(dy, x, weight, mean, rstd, kind="layer", bias=False, dx=True, stream=None):
-    """(dx, dweight, dbias) of norm_forward (moe_norm_backward); dweight is None without a weight, dbias
-    without bias (a truth value: whether its gradient is wanted), dx with dx=False."""
+def norm_backward(dy, x, weight, mean, rstd, kind="layer", bias=False, dx=True, dweight=True, stream=None):
+    """(dx, dweight, dbias) of norm_forward (moe_norm_backward).  dx, dweight and bias (for dbias) say which are
+    wanted; the others, and dweight without a weight, are None."""
     with _place(x, "x", stream):
         dev = x.get_device()
         px, ldx, rows, cols = _rows(x, "x")
@@ -558,7 +558,7 @@ def norm_backward(dy, x, weight, mean, rstd, kind="layer", bias=False, dx=True, 
         dt = _code(_DTYPE, x.dtype, "x.dtype")
         wd = weight.dtype if weight is not None else x.dtype
         gx = torch.empty_like(x, memory_format=torch.contiguous_format) if dx else None
-        gw = torch.empty(cols, dtype=wd, device=x.device) if weight is not None else None
+        gw = torch.empty(cols, dtype=wd, device=x.device) if dweight and weight is not None else None
         gb = torch.empty(cols, dtype=wd, device=x.device) if bias else None
         if gx is None and gw is None and gb is None:
             return None, None, None
@@ -594,10 +594,10 @@ class _Norm(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         want = ctx.needs_input_grad
-        gx, gw, gb = norm_backward(_row_major(dy), x, weight, mean, rstd, ctx.kind, bias=want[2], dx=want[0])
+        gx, gw, gb = norm_backward(_row_major(dy), x, weight, mean, rstd, ctx.kind, bias=want[2], dx=want[0], dweight=want[1])
         if gb is not None:
             gb = gb.to(ctx.bias_dtype)   # another dtype only where there is no weight to set it
-        return gx, gw if want[1] else None, gb, None, None
+        return gx, gw, gb, None, None
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5):
