@@ -213,6 +213,10 @@ def check_experts(s, x, idx, tw, w1, w2, ws=None):
     (100, 256, 128, 1, 1, 1, 128, False, 0),    # one expert
     (33, 256, 128, 300, 200, 8, 32, False, 50),
     (130, 1152, 128, 4, 2, 3, 128, True, 1),
+    (3, 256, 128, 40, 20, 17, 32, True, 5),     # more slots than a workgroup takes at once
+    (2, 640, 2048, 12, 9, 9, 32, False, 3),
+    (1, 128, 2176, 8, 8, 2, 128, True, 0),      # the shortest and longest K on either side of the token kernel
+    (20, 512, 128, 160, 160, 8, 64, True, 0),   # by pair, with more waves than are resident
 ])
 def test_experts(T, H, I, E, EL, k, group, zeros, e_lo, dtype):
     check_experts(*experts_inputs(T, H, I, E, EL, k, group, dtype, zeros, e_lo, seed=T))

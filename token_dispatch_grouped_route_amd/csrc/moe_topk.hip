@@ -16,10 +16,12 @@
 // and removing a row's best took 33 us for 65536 x 384 bf16 logits (top 6), whose bytes move in 11 us.
 // So a score and its id become one 32-bit key, the score's order-preserving bits with the id (inverted:
 // ties go to the lower) in the low bits, and a lane keeps its four largest keys sorted: a compare and
-// exchange is a min and a max, and a round is a maximum over the heads of the row's lanes and a pop.
+// exchange is a min and a max, and a round is a maximum over the heads of the row's lanes and a pop:
+// 17 us for those logits; 65536 x 256, top 8: bf16 with a bias 20 us, fp32 with 8 groups 31 us.  A lane whose four keys were all
+// taken makes its list anew from what is below the last one.
 // The key drops score bits where the id needs them.  16-bit logits without a bias have none there; else
-// two neighbours of the sorted result that agree in all remaining bits (or a lane whose four keys were
-// all taken) send the wave through the exact rounds on pairs.
+// the rounds go on while two neighbours agree in all bits kept, and the keys taken are then ranked by
+// their scores and ids (exact rounds on pairs only where there are more of them than lanes).
 #include <type_traits>
 
 #include "moe_vec.h"

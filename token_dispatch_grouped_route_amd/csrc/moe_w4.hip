@@ -11,10 +11,16 @@
 // enters in fp32 after each group, so no product is rounded before it.
 //
 // A wave reads 16 weight rows x 128 k at a time, 16 bytes (32 codes of one row) per lane: 64
-// contiguous bytes per row and instruction.  Two half-wave swaps and two 16-lane swaps transpose the
-// 4 x 4 dwords of the four lane groups, so MFMA i of the chunk takes k = 32 i .. 32 i + 31 (any group
-// size that is a multiple of 32 then ends between two MFMAs).  The waves of a workgroup split K and
-// their sums are added through LDS in wave order: no atomics, the same bits on every run.
+// contiguous bytes per row and instruction, two such steps in flight (three and four measured the same
+// at best, and 15% slower where more waves hide the latency).  Two half-wave swaps and two 16-lane swaps
+// transpose the 4 x 4 dwords of the four lane groups, so MFMA i of the chunk takes k = 32 i .. 32 i + 31
+// (any group size that is a multiple of 32 then ends between two MFMAs).  A team of waves splits K, and
+// its sums are added through LDS in wave order: no atomics, the same bits on every run.
+//
+// Reached: 64 tokens through 32 experts of 7168 x 4096 and back, groups of 32: 175 to 199 us for 730 MB
+// of codes, scales and zero points; one token through 6 of 2048 x 2816 and back: 18 us for 27 MB.  A small
+// call is bound by its steps in turn: in that one's L1 (9.8 us) the ids take 0.9 us, the first codes 2.1,
+// the other steps 4.3, joining and SwiGLU 0.5, and the slowest workgroup ends 2 later.
 #include <type_traits>
 
 #include "moe_vec.h"
@@ -407,6 +413,54 @@ __global__ __launch_bounds__(64 * TEAMS * KS, 2) void w4_experts_kernel(W4Expert
     }
 }
 
+// L2 and the combine of one token (grid y) in one launch: a wave per slot, TEAMS slots at a time, one tile of
+// output columns; y = the sum of w o over the token's local slots, in slot order.
+template <typename T, int FLUSH, bool ZEROS, int TEAMS>
+__global__ __launch_bounds__(64 * TEAMS, 2) void w4_token_kernel(W4Experts a) {
+    extern __shared__ __align__(16) unsigned char lds_raw[];
+    __shared__ float part[TEAMS][16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int K = a.I, groups = K >> a.gshift, stride = w4_stride(groups), col0 = blockIdx.x * 16;
+    unsigned char* lds = lds_raw + wave * w4_team_bytes<1, 1, ZEROS>(groups);
+    uint16_t* scales = reinterpret_cast<uint16_t*>(lds);
+    uint8_t* zeros = lds + 16 * stride * 2;
+    float y = 0.0f;
+    for (int j0 = 0; j0 < a.k; j0 += TEAMS) {
+        const int slots = min(TEAMS, a.k - j0);
+        const int64_t pair = static_cast<int64_t>(blockIdx.y) * a.k + j0 + min(wave, slots - 1);
+        const int e = __builtin_amdgcn_readfirstlane(a.topk_idx[pair]) - a.e_lo;
+        float v = 0.0f;
+        if (wave < slots && e >= 0 && e < a.EL) {
+            const int64_t row = static_cast<int64_t>(e) * a.H + col0;
+            W4Operands<1> o;
+            W4Meta<1, ZEROS, 1> meta;
+            o.K = K;
+            o.gshift = a.gshift;
+            o.wrow = (lane & 15) * (K >> 1) + 16 * (lane >> 4);
+            o.xrow = (w4_row() == 0 ? 0 : kNoRow) + 16 * (lane >> 4);
+            o.codes[0] = buffer_of(a.w2 + row * (K >> 1), 16 * (K >> 1));
+            o.x = buffer_of(static_cast<const T*>(a.act) + pair * K, 2 * K);
+            meta.groups = groups;
+            meta.rows[0] = 16;
+            meta.src[0] = static_cast<const uint16_t*>(a.s2) + row * groups;
+            meta.zsrc[0] = ZEROS ? a.z2 + row * groups : nullptr;
+            meta.load();
+            f32x4_t sum[1] = {};
+            w4_sums<T, 1, FLUSH, ZEROS, 1, true, true>(o, 0, scales + (lane & 15) * stride, zeros + (lane & 15) * stride, sum, [&] {
+                meta.store(scales, zeros);
+                wave_sync();
+            });
+            v = a.topk_w[pair] * sum[0][0];
+        }
+        if (lane < 16) part[wave][lane] = v;
+        lds_barrier();
+        if (threadIdx.x < 16)
+            for (int j = 0; j < slots; ++j) y += part[j][threadIdx.x];
+        lds_barrier();   // the next slots write part
+    }
+    if (threadIdx.x < 16) static_cast<T*>(a.y)[static_cast<int64_t>(blockIdx.y) * a.H + col0 + threadIdx.x] = from_f32<T>(y);
+}
+
 // y[t] = the sum of the token's local pairs' rows, in slot order (0 with none).
 template <typename T>
 __global__ __launch_bounds__(256) void w4_finish_kernel(W4Experts a) {
@@ -520,6 +574,15 @@ template <typename T, bool L1, int NT, int TEAMS, int KS> hipError_t run_experts
     return err;
 }
 
+constexpr int kTokenSlots = 8;   // waves of a workgroup of w4_token_kernel
+template <typename T> hipError_t run_token(const W4Experts& a, hipStream_t s) {
+    hipError_t err = hipSuccess;
+    with_group(1 << a.gshift, a.z2 != nullptr, [&](auto flush, auto zeros) {
+        err = launch_w4(&w4_token_kernel<T, flush(), zeros(), kTokenSlots>, dim3(a.H / 16, a.T), 64 * kTokenSlots,
+                        w4_lds<1, kTokenSlots, 1>(a.I >> a.gshift, zeros()), a, s);
+    });
+    return err;
+}
 template <typename T> hipError_t run_forward(const W4Experts& a, hipStream_t s) {
     const int pairs = a.T * a.k, slots = pairs < a.EL ? pairs : a.EL;
     // L1.  One row or so per expert: 2 + 2 tiles a workgroup (8 experts of 7168 x 4096 and back: 57 us; four
@@ -535,6 +598,10 @@ template <typename T> hipError_t run_forward(const W4Experts& a, hipStream_t s) 
     else if (w4_lds<2, 2, 2>(g1, z1) + list <= kLdsBytes / 2) e = run_experts<T, true, 2, 2, 2>(a, s);
     else e = run_experts<T, true, 2, 1, 4>(a, s);
     if (e != hipSuccess) return e;
+    // L2 with the combine, by token, while every wave of it is resident at once (16 a CU) and K is short for one
+    // wave (6 experts of 1408 x 2048: one token 20 against 22 us, two 23 against 30, four 39 against 44; eight
+    // 62 against 60.5, and one token through 6 of 4096 x 2048: 35 against 30 us).
+    if (static_cast<int64_t>(pairs) * (a.H / 16) <= 4096 && a.I <= 2048) return run_token<T>(a, s);
     // L2.  Independent waves of two tiles, which need no joining, once there are enough of them (8 experts:
     // 57 us against 64 us with one tile split over four waves; 6 experts of 1408 x 2048: 25 against 22 us).
     const int g2 = a.I >> a.gshift;
