@@ -1,5 +1,6 @@
 // Row norm, forward (layer norm and RMS norm): moe_norm.h has the formulas and the plan.  The variance is
 // a sum of centred squares, at no extra read since the row is in registers.
+// Layer norm of 8192 x 7168 bf16: 41 us (5.8 TB/s); rms norm of 65536 x 7168: 370 us (5.1 TB/s), one row: 4 us.
 #include "moe_norm.h"
 
 namespace moe {
@@ -83,7 +84,9 @@ __global__ __launch_bounds__(norm_block(TPR)) void norm_fwd_kernel(NormArgs a, b
     }
 }
 
-constexpr int kMost = 4;   // chunks per thread
+// Chunks per thread.  With 2, teams of twice the threads: 4000 x 12000 bf16 44 against 34 us, 20000 x 4001 76
+// against 69; 65536 x 7168 366 against 371, 1003 x 5001 fp32 10.9 against 11.8.
+constexpr int kMost = 4;
 
 hipError_t launch_norm_fwd(const NormArgs& a, int dtype, int wdtype, bool layer, hipStream_t s) {
     if (a.rows <= 0) return hipSuccess;

@@ -2,6 +2,8 @@
 // formulas and the plan.  A thread sums its columns' dy xh and dy over its team's rows in fp32; the teams
 // of a workgroup are joined in LDS, a workgroup leaves one partial row of dw and db, and a second launch
 // sums those, all in a fixed order: no atomics, the same bits on every run.
+// RMS norm of 65536 x 7168 bf16: 553 + 6 us (5.1 TB/s); layer norm of 1003 x 5001 fp32: 14 + 4 us, of 8192 x
+// 7168 bf16: 74 us.
 #include "moe_norm.h"
 
 namespace moe {
@@ -127,6 +129,7 @@ __global__ __launch_bounds__(norm_block(TPR)) void norm_bwd_kernel(NormArgs a) {
 
 // dw and db: the sum over the partial rows, 64 columns a workgroup: 16 lanes of four columns by 64 groups
 // of rows (group i takes rows i, i + 64, ...), then the groups are added in order.  No rows: zeros.
+// 512 rows of 7168: 6.4 us, most of it the latency of eight loads in flight and a launch.
 constexpr int kReduceGroups = 64;
 template <typename WT>
 __global__ __launch_bounds__(16 * kReduceGroups) void norm_reduce_kernel(const float* __restrict__ part_w, const float* __restrict__ part_b,
