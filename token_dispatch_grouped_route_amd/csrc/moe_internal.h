@@ -230,6 +230,7 @@ struct W4Experts {
     float* stage;   // [T * k, H] weighted L2 rows
     void* y;
     int32_t list_at;   // byte offset of the pair list in LDS (set at the launch)
+    int32_t passes;    // workgroups among which an expert's passes of 16 rows are dealt out (set at the launch)
 };
 constexpr int kW4MaxPairs = 4096;   // T * k of moe_forward_w4
 hipError_t launch_w4_linear(const W4Linear& a, int dtype, hipStream_t s);

@@ -17,7 +17,7 @@
 // (any group size that is a multiple of 32 then ends between two MFMAs).  A team of waves splits K, and
 // its sums are added through LDS in wave order: no atomics, the same bits on every run.
 //
-// Reached: 64 tokens through 32 experts of 7168 x 4096 and back, groups of 32: 175 to 199 us for 730 MB
+// Reached: 64 tokens through 32 experts of 7168 x 4096 and back, groups of 32: 170 to 190 us for 730 MB
 // of codes, scales and zero points; one token through 6 of 2048 x 2816 and back: 18 us for 27 MB.  A small
 // call is bound by its steps in turn: in that one's L1 (9.8 us) the ids take 0.9 us, the first codes 2.1,
 // the other steps 4.3, joining and SwiGLU 0.5, and the slowest workgroup ends 2 later.
@@ -323,7 +323,8 @@ __global__ __launch_bounds__(64 * TEAMS * KS, 2) void w4_linear_kernel(W4Linear 
 
 // ---------------------------------------------------------------------------------------------
 // Expert layer.  Grid y: with at most EL pairs, one workgroup row per pair, of which the first pair
-// of each expert works and the others leave; with more, one per local expert.  A workgroup lists its
+// of each expert works and the others leave; with more, one per local expert.  Grid x: tiles of columns, and
+// for each (on one XCD, as above) the workgroups that share an expert's passes of 16 rows.  A workgroup lists its
 // expert's pairs in ascending order itself (the ids are a few KB), so no table is built beforehand.
 // ---------------------------------------------------------------------------------------------
 // The pairs of expert id, ascending, and their number; 0 if `first` >= 0 and an earlier pair has it.  Every
@@ -331,13 +332,20 @@ __global__ __launch_bounds__(64 * TEAMS * KS, 2) void w4_linear_kernel(W4Linear 
 __device__ __forceinline__ int w4_pairs(const W4Experts& a, int id, int first, int* list) {
     const int pairs = a.T * a.k, lane = threadIdx.x & 63;
     int count = 0, earliest = pairs;
-    for (int p0 = 0; p0 < pairs; p0 += 64) {
-        const int p = p0 + lane;
-        const bool mine = p < pairs && a.topk_idx[p] == id;
-        const uint64_t m = __ballot(mine);
-        if (mine) list[count + __popcll(m & ((uint64_t(1) << lane) - 1))] = p;
-        if (m != 0 && count == 0) earliest = p0 + __ffsll(static_cast<unsigned long long>(m)) - 1;
-        count += __popcll(m);
+    constexpr int AHEAD = 8;   // loads in flight
+    for (int p0 = 0; p0 < pairs; p0 += 64 * AHEAD) {
+        int ids[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) ids[i] = a.topk_idx[min(p0 + 64 * i + lane, pairs - 1)];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int p = p0 + 64 * i + lane;
+            const bool mine = p < pairs && ids[i] == id;
+            const uint64_t m = __ballot(mine);
+            if (mine) list[count + __popcll(m & ((uint64_t(1) << lane) - 1))] = p;
+            if (m != 0 && count == 0) earliest = p0 + 64 * i + __ffsll(static_cast<unsigned long long>(m)) - 1;
+            count += __popcll(m);
+        }
     }
     wave_sync();   // the list is read by other lanes than those that wrote it
     return earliest < first ? 0 : count;
@@ -353,13 +361,14 @@ __global__ __launch_bounds__(64 * TEAMS * KS, 2) void w4_experts_kernel(W4Expert
     int* list = reinterpret_cast<int*>(lds_raw + a.list_at);
     const bool by_pair = pairs <= a.EL;
     const int id = by_pair ? __builtin_amdgcn_readfirstlane(a.topk_idx[blockIdx.y]) : a.e_lo + static_cast<int>(blockIdx.y), e = id - a.e_lo;
-    if (e < 0 || e >= a.EL) return;
-    const int count = w4_pairs(a, id, by_pair ? static_cast<int>(blockIdx.y) : -1, list);
-    if (count == 0) return;
+    constexpr int OUT = L1 ? 8 * NT : 16 * NT;   // output columns of a team: L1's first NT / 2 tiles are the gate's, the others the up's
+    const uint32_t passes = a.passes, b = blockIdx.x >> 3, pass = b % passes, block = b / passes * 8 + (blockIdx.x & 7);
+    const int col0 = (block * TEAMS + team) * OUT, columns = L1 ? a.I : a.H;
+    if (e < 0 || e >= a.EL || static_cast<int>(block * TEAMS) * OUT >= columns) return;
+    const int count = w4_pairs(a, id, by_pair ? static_cast<int>(blockIdx.y) : -1, list), m_first = 16 * pass;
+    if (m_first >= count) return;
 
     const int K = L1 ? a.H : a.I, groups = K >> a.gshift, stride = w4_stride(groups);
-    constexpr int OUT = L1 ? 8 * NT : 16 * NT;   // output columns of a team: L1's first NT / 2 tiles are the gate's, the others the up's
-    const int col0 = (blockIdx.x * TEAMS + team) * OUT, columns = L1 ? a.I : a.H;
     const int64_t wbase = static_cast<int64_t>(e) * (L1 ? 2 * a.I : a.H);   // first row of the expert
     unsigned char* lds = lds_raw + team * w4_team_bytes<NT, KS, ZEROS>(groups);
     uint16_t* scales = reinterpret_cast<uint16_t*>(lds);
@@ -381,7 +390,7 @@ __global__ __launch_bounds__(64 * TEAMS * KS, 2) void w4_experts_kernel(W4Expert
     }
     o.wrow = (lane & 15) * (K >> 1) + 16 * (lane >> 4);
     o.x = buffer_of(L1 ? a.x : a.act, static_cast<int64_t>(L1 ? a.T : pairs) * (2 * K));
-    for (int m0 = 0; m0 < count; m0 += 16) {
+    for (int m0 = m_first; m0 < count; m0 += 16 * passes) {
         meta.load();
         const int m = m0 + w4_row();
         o.xrow = (m < count ? static_cast<uint32_t>(L1 ? list[m] / a.k : list[m]) * (2 * K) : kNoRow) + 16 * (lane >> 4);
@@ -558,6 +567,9 @@ template <typename T, int NT, int TEAMS, int KS> hipError_t run_linear(const W4L
 template <int NT, int TEAMS, int KS> int w4_lds(int groups, bool zeros) {
     return TEAMS * (zeros ? w4_team_bytes<NT, KS, true>(groups) : w4_team_bytes<NT, KS, false>(groups));
 }
+// Passes of 16 rows that an expert of mean load makes.
+inline int w4_passes(const W4Experts& a) { return (a.T * a.k + 16 * a.EL - 1) / (16 * a.EL); }
+constexpr int kPassGroups = 512;   // two a CU; 1024 and 2048 measured within 5%, but 300 tokens through 16 of 4096 x 4096 217 against 188 us
 template <typename T, bool L1, int NT, int TEAMS, int KS> hipError_t run_experts(W4Experts a, hipStream_t s) {
     hipError_t err = hipSuccess;
     const int K = L1 ? a.H : a.I, columns = L1 ? a.I : a.H, pairs = a.T * a.k;
@@ -569,8 +581,15 @@ template <typename T, bool L1, int NT, int TEAMS, int KS> hipError_t run_experts
             err = hipErrorInvalidValue;
             return;
         }
-        err = launch_w4(&w4_experts_kernel<T, L1, NT, flush(), zeros(), TEAMS, KS>, dim3((columns + per - 1) / per, pairs < a.EL ? pairs : a.EL),
-                        64 * TEAMS * KS, lds, a, s);
+        // An expert's passes go to workgroups of their own while these are few (101 tokens, 6 of 8 experts of 1408
+        // x 1280 and back: 91 to 61 us; 256 tokens, 32 of 256 experts of 7168 x 4096, where most would only look
+        // for pairs: 270 to 771 us).
+        int blocks = (columns + per - 1) / per;
+        const int even = (blocks + 7) / 8 * 8, room = kPassGroups / (even * a.EL);
+        a.passes = w4_passes(a) < room ? w4_passes(a) : room;
+        if (a.passes > 1) blocks = even * a.passes;
+        else a.passes = 1;
+        err = launch_w4(&w4_experts_kernel<T, L1, NT, flush(), zeros(), TEAMS, KS>, dim3(blocks, pairs < a.EL ? pairs : a.EL), 64 * TEAMS * KS, lds, a, s);
     });
     return err;
 }
@@ -606,7 +625,7 @@ template <typename T> hipError_t run_forward(const W4Experts& a, hipStream_t s) 
     // L2.  Independent waves of two tiles, which need no joining, once there are enough of them (8 experts:
     // 57 us against 64 us with one tile split over four waves; 6 experts of 1408 x 2048: 25 against 22 us).
     const int g2 = a.I >> a.gshift;
-    if (static_cast<int64_t>(slots) * (a.H / 16) >= 2048 && w4_lds<2, 4, 1>(g2, z2) + list <= kLdsBytes / 2) e = run_experts<T, false, 2, 4, 1>(a, s);
+    if (static_cast<int64_t>(slots) * w4_passes(a) * (a.H / 16) >= 2048 && w4_lds<2, 4, 1>(g2, z2) + list <= kLdsBytes / 2) e = run_experts<T, false, 2, 4, 1>(a, s);
     else e = run_experts<T, false, 1, 1, 4>(a, s);
     if (e != hipSuccess) return e;
     w4_finish_kernel<T><<<dim3((a.H / 4 + 255) / 256, a.T), 256, 0, s>>>(a);
