@@ -470,7 +470,7 @@ __global__ __launch_bounds__(64 * TEAMS, 2) void w4_token_kernel(W4Experts a) {
     if (threadIdx.x < 16) static_cast<T*>(a.y)[static_cast<int64_t>(blockIdx.y) * a.H + col0 + threadIdx.x] = from_f32<T>(y);
 }
 
-// y[t] = the sum of the token's local pairs' rows, in slot order (0 with none).  Latency: 64 x 7168, 8 slots: 4.6 us.
+// y[t] = the sum of the token's local pairs' rows, in slot order (0 with none).  Latency: 64 x 7168, 8 slots: 4.9 us.
 template <typename T>
 __global__ __launch_bounds__(256) void w4_finish_kernel(W4Experts a) {
     const int c = (blockIdx.x * 256 + threadIdx.x) * 4, t = blockIdx.y;
