@@ -360,7 +360,7 @@ int32_t moe_mx_gemm2_combine(const moe_shape* shape, const uint8_t* w2q, const u
  */
 typedef enum moe_dtype { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
 typedef enum moe_norm_kind { MOE_LAYER_NORM = 0, MOE_RMS_NORM = 1 } moe_norm_kind;
-typedef enum moe_score { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
+typedef enum moe_score { MOE_SOFTMAX = 0, MOE_SIGMOID = 1, MOE_CHOOSE_BY_SCORE = 0x100 /* a flag, added to one of the two */ } moe_score;
 
 /*
  * Row norm.  Per row of x, with mean = sum x / cols (layer norm; 0 for RMS norm) and
@@ -397,12 +397,17 @@ int32_t moe_norm_backward(int32_t kind, int32_t dtype, int32_t wdtype, int64_t r
 /*
  * Router ("Mega MoE" page, Key points: the layer takes the routing as an input; this makes it).  Per
  * row of logits [device] dtype [T, E] (leading dimension ld):
- *   l = min(logit, largest fp32); an expert whose logit is NaN or -inf is out of service, as is one
- *   whose score s = l + bias is NaN or -inf (bias [device] fp32 [E], may be NULL; it takes part in
- *   the choice only).
+ *   l = min(logit, largest fp32); an expert whose logit is NaN or -inf is out of service.
+ *   The choice goes by s = v + bias (bias [device] fp32 [E], may be NULL; it takes part in the choice only),
+ *   an expert whose s is NaN or -inf not being chosen.  v is the logit l; with MOE_CHOOSE_BY_SCORE in `score`
+ *   (MOE_SIGMOID | MOE_CHOOSE_BY_SCORE) it is the expert's score: 1 / (1 + exp(-l)), resp. exp(l) over the
+ *   sum of exp(l) of all experts in service.  Routers that balance their experts by a bias on sigmoid scores,
+ *   and limit the choice to groups by those, are trained with the choice by score: with a bias or groups
+ *   the two differ.  Without either they are the same order, and the logits decide it (scores that fp32 no longer
+ *   tells apart would tie: a sigmoid is 1 from a logit of about 17 on; with a bias or groups they do).
  *   n_group > 1: the experts form n_group equal groups of consecutive ids; the topk_group groups of
- *   the largest sum of their two best scores stay (one expert in service: its score; ties: lower group).
- *   topk_idx [device] int32 [T, k]: the k largest scores, descending, ties to the lower id; -1 in the
+ *   the largest sum of their two best s stay (one expert to choose: its s; ties: lower group).
+ *   topk_idx [device] int32 [T, k]: the k largest s, descending, ties to the lower id; -1 in the
  *   slots for which no expert is left (moe_route_prologue ignores such ids).
  *   topk_w [device] fp32 [T, k]: scale * p, 0 in those slots, with p = exp(l) (MOE_SOFTMAX) divided by
  *   its sum over the chosen experts (renormalize != 0) or over all in service, or p = 1 / (1 + exp(-l))
@@ -415,7 +420,7 @@ int32_t moe_route_topk(int32_t dtype, int32_t T, int32_t E, int32_t k, const voi
 
 /*
  * Gradient of topk_w with respect to the logits, for the choice that moe_route_topk made (topk_idx; the
- * choice itself has no gradient, nor has bias): dlogits [device] dtype [T, E] (leading dimension ldd),
+ * choice itself has no gradient, nor has bias; `score` with or without MOE_CHOOSE_BY_SCORE): dlogits [device] dtype [T, E] (leading dimension ldd),
  * every element written.  dtopk_w [device] fp32 [T, k]; slots with an id outside [0, E) are ignored.
  * dlogits must not overlap logits.
  */

@@ -147,3 +147,11 @@ def test_without_a_gpu_valid_calls_report_the_device():
     assert norm_fwd() == DEVICE and norm_bwd() == DEVICE and route() == DEVICE and route_bwd() == DEVICE
     assert quantize() == DEVICE and linear() == DEVICE
     assert forward(moe.make_shape(4, 256, 128, 8, 8, 2, block_m=64)) == DEVICE
+
+
+def test_route_choice_by_score_is_a_flag_of_the_score():
+    for good in (0x100, 0x101):
+        assert route(T=0, score=good, logits=None, idx=None, w=None) == 0
+        assert route_bwd(T=0, score=good, logits=None, idx=None, dw=None, out=None) == 0
+    for bad in (0x102, 0x200, 0x301, -1):
+        assert route(score=bad) == SHAPE and route_bwd(score=bad) == SHAPE

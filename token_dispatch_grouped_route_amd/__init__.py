@@ -456,6 +456,7 @@ def moe_layer(x, topk_idx, topk_w, w1p, w2p, shape, ws=None):
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _KIND = {"layer": 0, "rms": 1}
 _SCORE = {"softmax": 0, "sigmoid": 1}
+_CHOICE = {"logit": 0, "score": 0x100}   # MOE_CHOOSE_BY_SCORE
 _HERE_ALREADY = contextlib.nullcontext()
 
 
@@ -612,9 +613,11 @@ def rms_norm(x, weight=None, eps=1e-5):
 
 
 def route_topk(logits, k, bias=None, score="softmax", renormalize=True, n_group=1, topk_group=1, scale=1.0, topk_idx=None, topk_w=None,
-               stream=None):
+               stream=None, choice="logit"):
     """(topk_idx int32 [T, k], topk_w fp32 [T, k]) of router logits [T, E] (moe_route_topk): what moe_layer
-    and the forward entry points take as their routing.  `router` is the differentiable form."""
+    and the forward entry points take as their routing.  `router` is the differentiable form.  choice says
+    what bias is added to and groups are rated by: "logit", or "score", the sigmoid or the softmax over
+    all experts, as routers with a balancing bias are trained."""
     with _place(logits, "logits", stream):
         dev = logits.get_device()
         if logits.dim() != 2:
@@ -625,7 +628,7 @@ def route_topk(logits, k, bias=None, score="softmax", renormalize=True, n_group=
         if topk_w is None:
             topk_w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
         _check(lib().moe_route_topk(_code(_DTYPE, logits.dtype, "logits.dtype"), T, E, k, p, ld, _like(bias, torch.float32, "bias", (E,), dev),
-                                    _code(_SCORE, score, "score"), bool(renormalize), n_group, topk_group, scale,
+                                    _code(_SCORE, score, "score") | _code(_CHOICE, choice, "choice"), bool(renormalize), n_group, topk_group, scale,
                                     _like(topk_idx, torch.int32, "topk_idx", (T, k), dev), _like(topk_w, torch.float32, "topk_w", (T, k), dev),
                                     _handle(dev)), "moe_route_topk")
     return topk_idx, topk_w
@@ -652,8 +655,8 @@ class _Router(torch.autograd.Function):
     """route_topk, with route_topk_backward for the gradient of the logits."""
 
     @staticmethod
-    def forward(ctx, logits, k, bias, score, renormalize, n_group, topk_group, scale):
-        idx, w = route_topk(logits, k, bias, score, renormalize, n_group, topk_group, scale)
+    def forward(ctx, logits, k, bias, score, renormalize, n_group, topk_group, scale, choice):
+        idx, w = route_topk(logits, k, bias, score, renormalize, n_group, topk_group, scale, choice=choice)
         ctx.save_for_backward(logits, idx)
         ctx.how = score, renormalize, scale
         ctx.mark_non_differentiable(idx)
@@ -663,13 +666,13 @@ class _Router(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, _, dw):
         logits, idx = ctx.saved_tensors
-        return (route_topk_backward(logits, idx, dw.contiguous(), *ctx.how),) + (None,) * 7
+        return (route_topk_backward(logits, idx, dw.contiguous(), *ctx.how),) + (None,) * 8
 
 
-def router(logits, k, bias=None, score="softmax", renormalize=True, n_group=1, topk_group=1, scale=1.0):
+def router(logits, k, bias=None, score="softmax", renormalize=True, n_group=1, topk_group=1, scale=1.0, choice="logit"):
     """route_topk as an autograd op: (topk_idx, topk_w), topk_w differentiable in the logits.  Feeds
     moe_layer, whose backward hands d(topk_w) back."""
-    return _Router.apply(logits, k, bias, score, renormalize, n_group, topk_group, scale)
+    return _Router.apply(logits, k, bias, score, renormalize, n_group, topk_group, scale, choice)
 
 
 def w4_quantize(w, group=128, zeros=False, dtype=None, stream=None):

@@ -566,7 +566,8 @@ int32_t moe_norm_backward(int32_t kind, int32_t dtype, int32_t wdtype, int64_t r
 namespace {
 int32_t check_route(int32_t dtype, int32_t T, int32_t E, int32_t k, int64_t ld, int32_t score) {
     if (!is_dtype(dtype) || T < 0 || T > kRouteMaxT || E < 1 || E > 1024 || k < 1 || k > 32 || k > E || bad_ld(ld, T, E)) return MOE_ERR_SHAPE;
-    return score == MOE_SOFTMAX || score == MOE_SIGMOID ? MOE_OK : MOE_ERR_SHAPE;
+    const int32_t kind = score & ~MOE_CHOOSE_BY_SCORE;
+    return kind == MOE_SOFTMAX || kind == MOE_SIGMOID ? MOE_OK : MOE_ERR_SHAPE;
 }
 }  // namespace
 
@@ -581,7 +582,8 @@ int32_t moe_route_topk(int32_t dtype, int32_t T, int32_t E, int32_t k, const voi
     if (!aligned_to(logits, dtype) || !aligned4(bias) || !aligned4(topk_idx) || !aligned4(topk_w)) return MOE_ERR_ALIGN;
     if (!is_gfx950()) return MOE_ERR_DEVICE;
     RouteArgs a = {};
-    a.T = T, a.E = E, a.k = k, a.n_group = n_group, a.topk_group = topk_group, a.sigmoid = score == MOE_SIGMOID;
+    a.T = T, a.E = E, a.k = k, a.n_group = n_group, a.topk_group = topk_group, a.sigmoid = (score & ~MOE_CHOOSE_BY_SCORE) == MOE_SIGMOID;
+    a.by_score = (score & MOE_CHOOSE_BY_SCORE) != 0 && (bias || n_group > 1);
     const int per_chunk = 16 / elem_bytes(dtype), chunks = E / n_group / per_chunk;
     a.group_shift = E / n_group % per_chunk == 0 && chunks <= 16 && (chunks & (chunks - 1)) == 0 ? __builtin_ctz(static_cast<unsigned>(chunks)) : -1;
     a.id_mask = 1;
@@ -602,7 +604,7 @@ int32_t moe_route_topk_backward(int32_t dtype, int32_t T, int32_t E, int32_t k, 
     if (!aligned_to(logits, dtype) || !aligned_to(dlogits, dtype) || !aligned4(topk_idx) || !aligned4(dtopk_w)) return MOE_ERR_ALIGN;
     if (!is_gfx950()) return MOE_ERR_DEVICE;
     RouteArgs a = {};
-    a.T = T, a.E = E, a.k = k, a.sigmoid = score == MOE_SIGMOID, a.renorm = renormalize != 0, a.scale = scale;
+    a.T = T, a.E = E, a.k = k, a.sigmoid = (score & ~MOE_CHOOSE_BY_SCORE) == MOE_SIGMOID, a.renorm = renormalize != 0, a.scale = scale;
     a.logits = logits, a.ld = ld, a.idx = topk_idx, a.dw = dtopk_w, a.dlogits = dlogits, a.ldd = ldd;
     return launched(launch_route_topk(a, dtype, true, static_cast<hipStream_t>(stream)));
 }

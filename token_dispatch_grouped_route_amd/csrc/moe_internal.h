@@ -197,6 +197,7 @@ struct RouteArgs {
     uint32_t id_mask;      // the smallest 2^b - 1 that holds every id
     int32_t group_shift;   // log2 of a group's 16-byte chunks of logits, if those are 1, 2, 4, 8 or 16; else -1
     bool sigmoid, renorm;
+    bool by_score;   // the choice goes by the scores: set where a bias or groups make it another than the logits'
     float scale;
     const void* logits;
     const float* bias;
