@@ -551,13 +551,18 @@ def norm_forward(x, weight=None, bias=None, eps=1e-5, kind="layer", y=None, stre
 
 def norm_backward(dy, x, weight, mean, rstd, kind="layer", bias=False, dx=True, dweight=True, stream=None):
     """(dx, dweight, dbias) of norm_forward (moe_norm_backward).  dx, dweight and bias (for dbias) say which are
-    wanted; the others, and dweight without a weight, are None."""
+    wanted; the others, and dweight without a weight, are None.  The gradients have the weight's dtype; without
+    a weight dbias has x's, or the one that bias names (x's or fp32)."""
     with _place(x, "x", stream):
         dev = x.get_device()
         px, ldx, rows, cols = _rows(x, "x")
         pdy, lddy = _rows(dy, "dy", x, x.shape)[:2]
         dt = _code(_DTYPE, x.dtype, "x.dtype")
-        wd = weight.dtype if weight is not None else x.dtype
+        named = bias if isinstance(bias, torch.dtype) else None
+        wd = weight.dtype if weight is not None else named or x.dtype
+        if named not in (None, wd):
+            raise MoeError("dbias in %s beside a weight in %s" % (named, wd))
+        bias = bool(bias) or named is not None
         gx = torch.empty_like(x, memory_format=torch.contiguous_format) if dx else None
         gw = torch.empty(cols, dtype=wd, device=x.device) if dweight and weight is not None else None
         gb = torch.empty(cols, dtype=wd, device=x.device) if bias else None
@@ -595,9 +600,7 @@ class _Norm(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         want = ctx.needs_input_grad
-        gx, gw, gb = norm_backward(_row_major(dy), x, weight, mean, rstd, ctx.kind, bias=want[2], dx=want[0], dweight=want[1])
-        if gb is not None:
-            gb = gb.to(ctx.bias_dtype)   # another dtype only where there is no weight to set it
+        gx, gw, gb = norm_backward(_row_major(dy), x, weight, mean, rstd, ctx.kind, bias=want[2] and ctx.bias_dtype, dx=want[0], dweight=want[1])
         return gx, gw, gb, None, None
 
 
