@@ -370,7 +370,8 @@ typedef enum moe_score { MOE_SOFTMAX = 0, MOE_SIGMOID = 1, MOE_CHOOSE_BY_SCORE =
  *                RMS norm takes no bias (MOE_ERR_SHAPE)
  *   mean, rstd   [device] fp32 [rows], written for the backward; either may be NULL; mean is not
  *                written for RMS norm
- * Statistics are fp32; a non-finite element makes its row non-finite.  rows >= 0 (0: nothing is done),
+ * Statistics are fp32; a non-finite element makes its row NaN, and so do elements whose (centred) squares sum to
+ * more than fp32 holds (all of about 2e17 at 7168 columns).  rows >= 0 (0: nothing is done),
  * cols 1 .. 32768, eps >= 0 (MOE_ERR_SHAPE otherwise).  Pointers need their element's alignment only.
  */
 int32_t moe_norm_forward(int32_t kind, int32_t dtype, int32_t wdtype, int64_t rows, int32_t cols, const void* x, int64_t ldx,

@@ -37,3 +37,30 @@ def test_a_bias_type_of_its_own_is_refused_beside_a_weight():
         with pytest.raises(moe.MoeError):
             moe.norm_backward(x, x, weight, mean, rstd, bias=kind)
     assert moe.norm_backward(x, x, w, mean, rstd, bias=torch.bfloat16)[2].dtype == torch.bfloat16
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("cols", [5, 1000, 7168])
+def test_rows_out_of_range_are_nan_and_stay_alone(cols, kind):
+    """Infinities, NaN and elements whose squares overflow make their own row NaN, forward and backward."""
+    inf = float("inf")
+    x = rows_of(gen(cols), 9, cols, torch.float32)
+    x[1, 0], x[2, cols - 1], x[3, cols // 2] = inf, -inf, float("nan")
+    x[4], x[4, ::2] = 1e25, -2e25
+    x[5, 0] = 3e38
+    x[6] = 0
+    x[7] *= 1e15                       # large, with squares that fit
+    bad = torch.zeros(9, dtype=torch.bool, device="cuda")
+    bad[1:6] = True
+    w = torch.full((cols,), 2.0, device="cuda")
+    b = torch.full((cols,), 0.5, device="cuda") if kind == "layer" else None
+    y, mean, rstd = moe.norm_forward(x, w, b, kind=kind)
+    assert torch.isnan(y[bad]).all() and torch.isnan(rstd[bad]).all()
+    check_forward(x[~bad].contiguous(), w, b, kind)
+    assert torch.equal(y[~bad], moe.norm_forward(x[~bad].contiguous(), w, b, kind=kind)[0])
+    dy = rows_of(gen(1), 9, cols, torch.float32)
+    dx, _, _ = moe.norm_backward(dy, x, w, mean, rstd, kind=kind)
+    assert torch.isnan(dx[bad]).all() and torch.isfinite(dx[~bad]).all()
+    if kind == "rms":
+        z = x.to(torch.bfloat16)
+        assert torch.isnan(moe.norm_forward(z, kind=kind)[0][bad]).all()

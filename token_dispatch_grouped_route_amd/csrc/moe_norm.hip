@@ -64,7 +64,9 @@ __global__ __launch_bounds__(norm_block(TPR)) void norm_fwd_kernel(NormArgs a, b
         }
         team_sum<TPR, 1>(q, lds + 2 * W, slot);
         slot ^= 1;
-        const float rstd = 1.0f / sqrtf(q[0] / static_cast<float>(cols) + a.eps);
+        // squares whose sum is not finite (an infinity, or elements too large for fp32's range) would give rstd 0 and a
+        // row of zeros that nothing shows: NaN instead, here and so in the backward
+        const float rstd = q[0] < __builtin_inff() ? 1.0f / sqrtf(q[0] / static_cast<float>(cols) + a.eps) : __builtin_nanf("");
         if (row < a.rows) {
             if (tid == 0) {
                 if (layer && a.mean) a.mean[row] = mean;
