@@ -421,8 +421,9 @@ int32_t moe_route_topk(int32_t dtype, int32_t T, int32_t E, int32_t k, const voi
 
 /*
  * Gradient of topk_w with respect to the logits, for the choice that moe_route_topk made (topk_idx; the
- * choice itself has no gradient, nor has bias; `score` with or without MOE_CHOOSE_BY_SCORE): dlogits [device] dtype [T, E] (leading dimension ldd),
- * every element written.  dtopk_w [device] fp32 [T, k]; slots with an id outside [0, E) are ignored.
+ * choice itself has no gradient, nor has bias; `score` with or without MOE_CHOOSE_BY_SCORE): dlogits [device]
+ * dtype [T, E] (leading dimension ldd), every element written.  dtopk_w [device] fp32 [T, k]; slots with an id
+ * outside [0, E) are ignored, the gradients of slots that name the same expert are added in slot order.
  * dlogits must not overlap logits.
  */
 int32_t moe_route_topk_backward(int32_t dtype, int32_t T, int32_t E, int32_t k, const void* logits, int64_t ld,

@@ -399,7 +399,7 @@ __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
     }
 }
 
-// The gradients of the chosen go through a row of LDS, where lane j adds slot j's and every lane then
+// The gradients of the chosen go through a row of LDS, where lane j puts slot j's and every lane then
 // reads its chunks' (comparing each element's id with each slot's took 270 instructions a wave, and 65536
 // x 250 bf16 logits 22 us, against 13; bound by memory where it is dense: 65536 x 256 fp32 25 us, 5.5 TB/s).
 // DENSE: softmax over all, where every expert in service has one.
@@ -455,8 +455,23 @@ __global__ __launch_bounds__(256) void route_topk_bwd_kernel(RouteArgs a) {
     float d = a.renorm ? p * (g - q) : p * g;
     if (a.sigmoid) d *= sigmoid_f32(-l);   // 1 - sigmoid(l)
     wave_sync();   // a row's LDS is its wave's alone
-    if (there) atomicAdd(mine + pick, d);
+    // Slots that name one expert (the router's never do) are added in slot order: who wrote last is seen from what
+    // the place holds, and only then do the slots take turns.
+    if (there) mine[pick] = __int_as_float(lane);
     wave_sync();
+    const bool shared = there && __float_as_int(mine[pick]) != lane;
+    wave_sync();
+    if (there) mine[pick] = d;
+    wave_sync();
+    if (__ballot(shared) != 0) {
+        if (there) mine[pick] = 0.0f;
+        wave_sync();
+#pragma unroll 1
+        for (int n = 0; n < a.k; ++n) {
+            if (there && lane == n) mine[pick] += d;
+            wave_sync();
+        }
+    }
     const float share = DENSE && all_sum > 0.0f ? q / all_sum : 0.0f;
     T* dx = static_cast<T*>(a.dlogits) + r * a.ldd;
 #pragma unroll
