@@ -234,3 +234,27 @@ def test_refused_choice():
             moe.route_topk(l, 2, choice=bad)
         with pytest.raises(moe.MoeError):
             moe.router(l, 2, choice=bad)
+
+
+@pytest.mark.parametrize("choice", ["logit", "score"])
+def test_a_bias_of_minus_infinity_bars_from_the_choice_alone(choice):
+    """The softmax over all runs over every expert whose logit is usable, barred by its bias or not, and so does its
+    gradient; an expert whose logit is out of service has no part in either."""
+    E, k = 40, 5
+    l = logits_of(30, E, torch.float32, 11)
+    l[:, 7] = -float("inf")
+    bias = torch.zeros(E, device="cuda")
+    bias[::3] = -float("inf")
+    idx, w = moe.route_topk(l, k, bias=bias, renormalize=False, choice=choice)
+    assert (idx % 3 != 0).all() and (idx != 7).all() and (idx >= 0).all()
+    z = l.double().cpu().requires_grad_()
+    p = torch.softmax(z, 1).gather(1, idx.cpu().long())
+    # relative, at |l - m| < 10: two exponentials within 29 u, 46 additions
+    assert ((w.double().cpu() - p).abs() <= 110 * U * p).all()
+    free, _ = moe.route_topk(l[:, torch.arange(E, device="cuda") % 3 != 0].contiguous(), k)
+    assert torch.equal(free, idx - idx // 3 - 1)
+    up = torch.randn(30, k, generator=torch.Generator().manual_seed(2))
+    (p * up.double()).sum().backward()
+    got = moe.route_topk_backward(l, idx, up.cuda(), renormalize=False).double().cpu()
+    assert (got[:, 7] == 0).all() and (got[:, ::3] != 0).all()
+    assert ((got - z.grad).abs() <= 150 * U * 2 * up.double().abs().sum(1, keepdim=True)).all()
