@@ -234,6 +234,13 @@ struct W4Experts {
     int32_t passes;    // workgroups among which an expert's passes of 16 rows are dealt out (set at the launch)
 };
 constexpr int kW4MaxPairs = 4096;   // T * k of moe_forward_w4
+// Whether L2 runs by token, in one launch with the combine: while its T x H / 16 workgroups of eight waves are
+// resident at once (two a CU), whatever k is, and K is short for one wave.  Over 802 shapes (H x I 256 x 256 to 7168 x
+// 2048, 1 to 64 experts, top 1 to 8, 1 to 128 tokens, bf16) this is within 0.3% of always taking the faster way,
+// 16% at worst; bounds of 384 and 768 workgroups 1.6% and 0.8%, by expert alone 11%.  6 of 64 experts of 2048 x 1408: one
+// token 19.6 against 22.1 us, four 36 against 42, eight (beyond the bound) 59 against 57; 32 tokens on one such expert
+// (beyond) 55 against 22 us.  One token through 6 of 4096 x 2048, a K of 4096: 35 against 30 us.
+inline bool w4_by_token(int64_t T, int H, int I) { return T * (H / 16) <= 512 && I <= 2048; }
 hipError_t launch_w4_linear(const W4Linear& a, int dtype, hipStream_t s);
 hipError_t launch_w4_forward(const W4Experts& a, int dtype, hipStream_t s);
 hipError_t launch_w4_quantize(int wdtype, int dtype, int E, int K, int N, int group, const void* w, uint8_t* codes, void* scales,

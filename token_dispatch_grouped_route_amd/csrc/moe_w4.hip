@@ -423,7 +423,8 @@ __global__ __launch_bounds__(64 * TEAMS * KS, 2) void w4_experts_kernel(W4Expert
 }
 
 // L2 and the combine of one token (grid y) in one launch: a wave per slot, TEAMS slots at a time, one tile of
-// output columns; y = the sum of w o over the token's local slots, in slot order.
+// output columns; y = the sum of w o over the token's local slots, in slot order.  Tokens share no weights
+// here: an expert's W2 is read once per pair, from the caches but for the first.
 template <typename T, int FLUSH, bool ZEROS, int TEAMS>
 __global__ __launch_bounds__(64 * TEAMS, 2) void w4_token_kernel(W4Experts a) {
     extern __shared__ __align__(16) unsigned char lds_raw[];
@@ -618,10 +619,7 @@ template <typename T> hipError_t run_forward(const W4Experts& a, hipStream_t s) 
     else if (w4_lds<2, 2, 2>(g1, z1) + list <= kLdsBytes / 2) e = run_experts<T, true, 2, 2, 2>(a, s);
     else e = run_experts<T, true, 2, 1, 4>(a, s);
     if (e != hipSuccess) return e;
-    // L2 with the combine, by token, while every wave of it is resident at once (16 a CU) and K is short for one
-    // wave (6 experts of 1408 x 2048: one token 20 against 22 us, two 23 against 30, four 39 against 44; eight
-    // 62 against 60.5, and one token through 6 of 4096 x 2048: 35 against 30 us).
-    if (static_cast<int64_t>(pairs) * (a.H / 16) <= 4096 && a.I <= 2048) return run_token<T>(a, s);
+    if (w4_by_token(a.T, a.H, a.I)) return run_token<T>(a, s);
     // L2.  Independent waves of two tiles, which need no joining, once there are enough of them (8 experts:
     // 57 us against 64 us with one tile split over four waves; 6 experts of 1408 x 2048: 25 against 22 us).
     const int g2 = a.I >> a.gshift;
