@@ -64,3 +64,22 @@ def test_rows_out_of_range_are_nan_and_stay_alone(cols, kind):
     if kind == "rms":
         z = x.to(torch.bfloat16)
         assert torch.isnan(moe.norm_forward(z, kind=kind)[0][bad]).all()
+
+
+# the first chunk counts (16 bytes of a row each) of every team and every number of chunks a thread takes
+CHUNKS = [1] + [n for j in range(3, 13) for n in (2 ** j + 1, 3 * 2 ** (j - 1) + 1)] + [8192]
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("chunks,dtype", [(c, t) for t in (torch.bfloat16, torch.float16, torch.float32) for c in CHUNKS if c * 16 // t.itemsize <= 32768])
+def test_every_geometry(chunks, kind, dtype):
+    """Each (threads per row, chunks per thread) that a width selects, with several rows per team in the widest."""
+    per = 16 // dtype.itemsize
+    cols = chunks * per - (0 if chunks == 8192 else per // 2 - 1)
+    rows = 600 if chunks > 1024 else 9
+    g = gen(chunks)
+    x, dy = rows_of(g, rows, cols, dtype), rows_of(g, rows, cols, dtype)
+    w = (1 + 0.2 * torch.randn(cols, generator=g, device="cuda")).to(dtype)
+    b = (0.1 * torch.randn(cols, generator=g, device="cuda")).to(dtype) if kind == "layer" else None
+    _, mean, rstd = check_forward(x, w, b, kind)
+    check_backward(dy, x, w, mean, rstd, kind, kind == "layer")

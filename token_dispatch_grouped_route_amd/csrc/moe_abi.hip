@@ -490,7 +490,7 @@ int32_t moe_forward_mx(const moe_shape* shape, const uint8_t* xq, const uint8_t*
 // Operators around the expert layer: row norm, router, 4-bit products
 // ---------------------------------------------------------------------------------------------
 namespace {
-constexpr int kNormMaxCols = 32768, kW4MaxK = 32768;
+constexpr int kW4MaxK = 32768;
 constexpr int64_t kW4MaxLd = 1 << 23;   // 16 rows of x stay within 32-bit byte offsets
 constexpr int kRouteMaxT = 1 << 25;        // a grid has fewer than 2^32 threads: 64 per token,
 constexpr int64_t kW4MaxTiles = 1 << 23;   // and 256 per 16 x 16 tile of moe_w4_linear's y

@@ -177,6 +177,7 @@ hipError_t launch_mx_pack(const Dims& d, const uint16_t* w1, const uint16_t* w2,
                           uint8_t* w2q, uint8_t* w2s, hipStream_t s);
 
 // Row norm (moe_norm_forward / moe_norm_backward): y is dx in the backward.
+constexpr int kNormMaxCols = 32768;
 struct NormArgs {
     int64_t rows;
     int32_t cols;

@@ -92,33 +92,52 @@ template <typename WT, int N, int NV, int TPR> struct NormWeights {
 // Threads per row and chunks per thread: the smallest team of a power of two (8 to 1024) whose threads take
 // at most `most` chunks each; rows beyond 1024 x most, up to 32768 elements, take more.
 struct Geometry { int tpr, nv; };
-inline Geometry norm_geometry(int64_t chunks, int most) {
+constexpr Geometry norm_geometry(int64_t chunks, int most) {
     for (int tpr = 8; tpr <= 1024; tpr *= 2)
         if (chunks <= static_cast<int64_t>(tpr) * most) return {tpr, static_cast<int>((chunks + tpr - 1) / tpr)};
     const int nv = static_cast<int>((chunks + 1023) / 1024);
     return {1024, nv <= 4 ? nv : 8};
 }
-inline int64_t norm_chunks(int cols, int elem_bytes) { return (static_cast<int64_t>(cols) * elem_bytes + 15) / 16; }
+constexpr int64_t norm_chunks(int cols, int elem_bytes) { return (static_cast<int64_t>(cols) * elem_bytes + 15) / 16; }
 
 template <int TPR, int NV> struct Geo {
     static constexpr int tpr = TPR, nv = NV;
 };
-// Calls f with the compiled geometry: a team other than the smallest has over most / 2 chunks a thread.
-template <int TPR, int NV, typename F> bool is_geometry(const Geometry& g, F&& f) {
+template <int TPR, int NV, typename F> constexpr bool is_geometry(const Geometry& g, F&& f) {
     if (g.tpr != TPR || g.nv != NV) return false;
     f(Geo<TPR, NV>{});
     return true;
 }
-template <int MOST, int BYTES, typename F> void with_geometry(const Geometry& g, F&& f) {
-    auto team = [&](auto tpr) {
-        if constexpr (MOST == 2) return is_geometry<tpr(), 2>(g, f);
-        else return is_geometry<tpr(), 3>(g, f) || is_geometry<tpr(), 4>(g, f);
-    };
-    bool done = is_geometry<8, 1>(g, f) || (MOST > 2 && is_geometry<8, 2>(g, f)) || team(std::integral_constant<int, 8>{}) || team(std::integral_constant<int, 16>{}) ||
-                team(std::integral_constant<int, 32>{}) || team(std::integral_constant<int, 64>{}) || team(std::integral_constant<int, 128>{}) ||
-                team(std::integral_constant<int, 256>{}) || team(std::integral_constant<int, 512>{}) || team(std::integral_constant<int, 1024>{});
-    if constexpr (MOST == 2) done = done || is_geometry<1024, 3>(g, f) || is_geometry<1024, 4>(g, f);
-    if constexpr (BYTES == 4) done = done || is_geometry<1024, 8>(g, f);
+// A team of TPR threads has over MOST / 2 chunks a thread, the smallest any number.
+template <int TPR, int MOST, typename F> constexpr bool is_team(const Geometry& g, F&& f) {
+    if constexpr (MOST == 2) return is_geometry<TPR, 2>(g, f);
+    else return is_geometry<TPR, 3>(g, f) || is_geometry<TPR, 4>(g, f);
+}
+// Calls f with the compiled geometry; false if there is none.  LONG512: rows beyond 512 x MOST chunks stay with
+// 512 threads up to twice that (the layer norm's backward).
+template <int MOST, int BYTES, bool LONG512, typename F> constexpr bool with_geometry(const Geometry& g, F&& f) {
+    if (is_geometry<8, 1>(g, f) || (MOST > 2 && is_geometry<8, 2>(g, f)) || is_team<8, MOST>(g, f) || is_team<16, MOST>(g, f) || is_team<32, MOST>(g, f) ||
+        is_team<64, MOST>(g, f) || is_team<128, MOST>(g, f) || is_team<256, MOST>(g, f) || is_team<512, MOST>(g, f))
+        return true;
+    if constexpr (!LONG512) {
+        if (is_team<1024, MOST>(g, f)) return true;
+    } else if constexpr (MOST == 2) {
+        if (is_geometry<512, 3>(g, f) || is_geometry<512, 4>(g, f)) return true;
+    } else {
+        if (is_geometry<512, 6>(g, f) || is_geometry<512, 8>(g, f)) return true;
+    }
+    if constexpr (MOST == 2) {
+        if (is_geometry<1024, 3>(g, f) || is_geometry<1024, 4>(g, f)) return true;
+    }
+    if constexpr (BYTES == 4) return is_geometry<1024, 8>(g, f);
+    return false;
+}
+// Whether `pick` (chunks of a row to its geometry) finds a compiled one for every width of BYTES-byte elements.
+// A geometry holds for runs of 8 and more chunks that begin after a multiple of 8, so one of each is tried.
+template <int MOST, int BYTES, bool LONG512, typename P> constexpr bool every_width(P pick) {
+    for (int64_t c = 1; c <= norm_chunks(kNormMaxCols, BYTES); c += 8)
+        if (!with_geometry<MOST, BYTES, LONG512>(pick(c), [](auto) {})) return false;
+    return true;
 }
 
 template <typename F> void with_types(int dtype, int wdtype, F&& f) {

@@ -89,19 +89,22 @@ __global__ __launch_bounds__(norm_block(TPR)) void norm_fwd_kernel(NormArgs a, b
 // Chunks per thread.  With 2, teams of twice the threads: 4000 x 12000 bf16 44 against 34 us, 20000 x 4001 76
 // against 69; 65536 x 7168 366 against 371, 1003 x 5001 fp32 10.9 against 11.8.
 constexpr int kMost = 4;
+constexpr Geometry fwd_geometry(int64_t chunks) { return norm_geometry(chunks, kMost); }
+static_assert(every_width<kMost, 2, false>(fwd_geometry) && every_width<kMost, 4, false>(fwd_geometry), "a width without a kernel");
 
 hipError_t launch_norm_fwd(const NormArgs& a, int dtype, int wdtype, bool layer, hipStream_t s) {
     if (a.rows <= 0) return hipSuccess;
+    bool done = false;
     with_types(dtype, wdtype, [&](auto t, auto wt) {
         using T = decltype(t);
-        with_geometry<kMost, sizeof(T)>(norm_geometry(norm_chunks(a.cols, sizeof(T)), kMost), [&](auto geo) {
+        done = with_geometry<kMost, sizeof(T), false>(fwd_geometry(norm_chunks(a.cols, sizeof(T))), [&](auto geo) {
             using G = decltype(geo);
             constexpr int block = norm_block(G::tpr), teams = block / G::tpr;
             const int64_t want = (a.rows + teams - 1) / teams, cap = static_cast<int64_t>(device_cu_count()) * (2048 / block);
             norm_fwd_kernel<T, decltype(wt), G::tpr, G::nv><<<static_cast<int>(want < cap ? want : cap), block, 0, s>>>(a, layer);
         });
     });
-    return hipGetLastError();
+    return done ? hipGetLastError() : hipErrorInvalidConfiguration;
 }
 
 }  // namespace moe

@@ -161,53 +161,60 @@ __global__ __launch_bounds__(16 * kReduceGroups) void norm_reduce_kernel(const f
 // and the weights then leave three (layer norm) or four waves a SIMD (rms backward of 65536 x 7168 bf16: 545
 // to 555 us; with 32 elements, 588 to 630 us).  Layer norm rows of more than 512 x 16 elements take up to 32
 // in the same 512 threads (12000-wide: 72 us for 4000 rows; 1024 threads of 16 spill, 136 us).
-int64_t norm_bwd_layout(int64_t chunks, int elem_bytes, bool layer, Geometry* g) {
-    const int most = elem_bytes == 4 ? 4 : 2;
-    *g = norm_geometry(chunks, most);
-    if (layer && g->tpr == 1024 && chunks <= 512 * 2 * most) *g = {512, static_cast<int>((chunks + 511) / 512)};
-    if (elem_bytes == 4 && g->tpr == 512 && g->nv > 4) g->nv = g->nv <= 6 ? 6 : 8;
-    return layer ? (g->tpr <= 256 ? 3 : 1) : g->tpr <= 256 ? 4 : g->tpr == 512 ? 2 : 1;   // workgroups a CU holds
+// Rows of more than 12288 elements spill registers (the layer norm's, and fp32 RMS): 2000 x 14000 fp32 151 us for
+// layer norm, 92 for RMS, 4000 x 14000 bf16 96 and 70, with 69 us of bytes to move.  Above 16384 elements, where 1024
+// threads with 128 registers each hold the row, the next row and the sums, scratch traffic is most of the time:
+// 1000 x 32768 fp32 690 and 540 us for 80 us of bytes, 2000 x 20000 bf16 layer norm 290 for 49.
+constexpr int bwd_most(int elem_bytes) { return elem_bytes == 4 ? 4 : 2; }
+constexpr Geometry bwd_geometry(int64_t chunks, int elem_bytes, bool layer) {
+    const int most = bwd_most(elem_bytes);
+    Geometry g = norm_geometry(chunks, most);
+    if (layer && g.tpr == 1024 && chunks <= 512 * 2 * most) g = {512, static_cast<int>((chunks + 511) / 512)};
+    if (elem_bytes == 4 && g.tpr == 512 && g.nv > 4) g.nv = g.nv <= 6 ? 6 : 8;
+    return g;
 }
+template <int BYTES, bool LAYER> constexpr bool every_bwd_width() {
+    return every_width<bwd_most(BYTES), BYTES, LAYER>([](int64_t chunks) { return bwd_geometry(chunks, BYTES, LAYER); });
+}
+static_assert(every_bwd_width<2, true>() && every_bwd_width<2, false>() && every_bwd_width<4, true>() && every_bwd_width<4, false>(), "a width without a kernel");
+// Workgroups a CU holds.
+constexpr int bwd_per_cu(const Geometry& g, bool layer) { return layer ? (g.tpr <= 256 ? 3 : 1) : g.tpr <= 256 ? 4 : g.tpr == 512 ? 2 : 1; }
 
 // Workgroups of the backward (each leaves one partial row of dw and db): what fills the chip, and at least
 // two rows a team, which halves the partial rows of a short batch.
 constexpr int kCus = 256;   // MI355X
 int64_t norm_bwd_slots(int64_t rows, int cols, int elem_bytes, bool layer) {
-    Geometry g;
-    const int64_t cap = kCus * norm_bwd_layout(norm_chunks(cols, elem_bytes), elem_bytes, layer, &g);
+    const Geometry g = bwd_geometry(norm_chunks(cols, elem_bytes), elem_bytes, layer);
+    const int64_t cap = kCus * bwd_per_cu(g, layer);
     const int teams = norm_block(g.tpr) / g.tpr;
     const int64_t want = (rows + 2 * teams - 1) / (2 * teams);
     return want < cap ? want : cap;
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, int dtype, int wdtype, bool layer, hipStream_t s) {
+    bool done = true;
     with_types(dtype, wdtype, [&](auto t, auto wt) {
         using T = decltype(t);
         using WT = decltype(wt);
-        constexpr int bytes = sizeof(T), most = bytes == 4 ? 4 : 2;
+        constexpr int bytes = sizeof(T), most = bwd_most(bytes);
         const int64_t slots = norm_bwd_slots(a.rows, a.cols, bytes, layer);
-        Geometry g;
-        norm_bwd_layout(norm_chunks(a.cols, bytes), bytes, layer, &g);
+        const Geometry g = bwd_geometry(norm_chunks(a.cols, bytes), bytes, layer);
         if (slots > 0 && layer) {
-            auto run = [&](auto geo) {
+            done = with_geometry<most, bytes, true>(g, [&](auto geo) {
                 using G = decltype(geo);
                 norm_bwd_kernel<T, WT, true, G::tpr, G::nv><<<static_cast<int>(slots), norm_block(G::tpr), 0, s>>>(a);
-            };
-            bool done;
-            if constexpr (bytes == 4) done = is_geometry<512, 6>(g, run) || is_geometry<512, 8>(g, run);
-            else done = is_geometry<512, 3>(g, run) || is_geometry<512, 4>(g, run);
-            if (!done) with_geometry<most, bytes>(g, run);
+            });
         } else if (slots > 0) {
-            with_geometry<most, bytes>(g, [&](auto geo) {
+            done = with_geometry<most, bytes, false>(g, [&](auto geo) {
                 using G = decltype(geo);
                 norm_bwd_kernel<T, WT, false, G::tpr, G::nv><<<static_cast<int>(slots), norm_block(G::tpr), 0, s>>>(a);
             });
         }
-        if (a.dweight || a.dbias)
+        if (done && (a.dweight || a.dbias))
             norm_reduce_kernel<WT><<<dim3((a.cols + 63) / 64, a.dbias ? 2 : 1), 16 * kReduceGroups, 0, s>>>(
                 a.part_w, a.part_b, slots, a.cols, static_cast<WT*>(a.dweight), static_cast<WT*>(a.dbias));
     });
-    return hipGetLastError();
+    return done ? hipGetLastError() : hipErrorInvalidConfiguration;
 }
 
 }  // namespace moe
