@@ -674,7 +674,7 @@ class _Router(torch.autograd.Function):
 
 def router(logits, k, bias=None, score="softmax", renormalize=True, n_group=1, topk_group=1, scale=1.0, choice="logit"):
     """route_topk as an autograd op: (topk_idx, topk_w), topk_w differentiable in the logits.  Feeds
-    moe_layer, whose backward hands d(topk_w) back."""
+    moe_layer, whose backward hands d(topk_w) back.  choice as for route_topk."""
     return _Router.apply(logits, k, bias, score, renormalize, n_group, topk_group, scale, choice)
 
 

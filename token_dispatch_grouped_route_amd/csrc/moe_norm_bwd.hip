@@ -2,7 +2,7 @@
 // formulas and the plan.  A thread sums its columns' dy xh and dy over its team's rows in fp32; the teams
 // of a workgroup are joined in LDS, a workgroup leaves one partial row of dw and db, and a second launch
 // sums those, all in a fixed order: no atomics, the same bits on every run.
-// RMS norm of 65536 x 7168 bf16: 553 + 6 us (5.1 TB/s); layer norm of 1003 x 5001 fp32: 14 + 4 us, of 8192 x
+// RMS norm of 65536 x 7168 bf16: 546 + 6 us (5.2 TB/s); layer norm of 1003 x 5001 fp32: 14 + 4 us, of 8192 x
 // 7168 bf16: 74 us.
 #include "moe_norm.h"
 
@@ -182,7 +182,7 @@ constexpr int bwd_per_cu(const Geometry& g, bool layer) { return layer ? (g.tpr 
 
 // Workgroups of the backward (each leaves one partial row of dw and db): what fills the chip, and at least
 // two rows a team, which halves the partial rows of a short batch.
-constexpr int kCus = 256;   // MI355X
+constexpr int kCus = 256;   // MI355X: a constant, so that the workspace's size follows from the sizes alone
 int64_t norm_bwd_slots(int64_t rows, int cols, int elem_bytes, bool layer) {
     const Geometry g = bwd_geometry(norm_chunks(cols, elem_bytes), elem_bytes, layer);
     const int64_t cap = kCus * bwd_per_cu(g, layer);

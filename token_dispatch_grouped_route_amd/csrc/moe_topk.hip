@@ -72,6 +72,8 @@ __device__ __forceinline__ void better(float& v, int& id, float ov, int oid) {
     if (ov > v || (ov == v && oid < id)) v = ov, id = oid;
 }
 
+// The weights are ratios of fast exponentials, off by (2.5 |a| + 4) 2^-24 relative at an argument a: 2^-20 for a
+// weight that is e^-5 of its row's largest, less than the products they scale are rounded by.
 __device__ __forceinline__ float sigmoid_f32(float l) {   // no overflow on either side
     const float e = __expf(-fabsf(l));
     return (l >= 0.0f ? 1.0f : e) / (1.0f + e);
