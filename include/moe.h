@@ -469,9 +469,10 @@ size_t moe_w4_workspace_bytes(const moe_shape* shape);
  * SwiGLU is applied in fp32 and the activation rounded to dtype; L2 sums, weights and combines in fp32
  * in slot order (the same bits on every run); y [device] dtype [T, H].  An expert's weights are read
  * once per 16 of its pairs; for the fewest tokens (T * H at most 8192, I at most 2048) w2's once per pair, by
- * workgroups that run at the same time and find them in the caches.  T * k at most 4096 (MOE_ERR_SHAPE): longer batches are for moe_forward and
- * moe_forward_mx, on weights in their formats.  shape->train must be 0; block_m is not used.  ws [device] 256-B aligned scratch, which calls
- * in flight at the same time (and graphs replayed at the same time) must not share.
+ * workgroups that run at the same time and find them in the caches.  T * k at most 4096 (MOE_ERR_SHAPE):
+ * longer batches are for moe_forward and moe_forward_mx, on weights in their formats.  shape->train must be 0;
+ * block_m is not used.  ws [device] 256-B aligned scratch, which calls in flight at the same time (and graphs
+ * replayed at the same time) must not share.
  */
 int32_t moe_forward_w4(const moe_shape* shape, int32_t dtype, int32_t group, const void* x, const int32_t* topk_idx,
                        const float* topk_w, const uint8_t* w1, const void* s1, const uint8_t* z1, const uint8_t* w2,

@@ -457,16 +457,17 @@ __global__ __launch_bounds__(256) void route_topk_bwd_kernel(RouteArgs a) {
     float d = a.renorm ? p * (g - q) : p * g;
     if (a.sigmoid) d *= sigmoid_f32(-l);   // 1 - sigmoid(l)
     wave_sync();   // a row's LDS is its wave's alone
-    // Slots that name one expert (the router's never do) are added in slot order: who wrote last is seen from what
-    // the place holds, and only then do the slots take turns.
-    if (there) mine[pick] = __int_as_float(lane);
+    // Slots that name one expert (the router's never do) are added in slot order: a slot sees from what its place
+    // holds whether another one claimed it too, and only then do the slots take turns.
+    auto claim = [&](float v) { __hip_atomic_store(mine + pick, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT); };
+    if (there) claim(__int_as_float(lane));
     wave_sync();
-    const bool shared = there && __float_as_int(mine[pick]) != lane;
+    const bool shared = there && __float_as_int(__hip_atomic_load(mine + pick, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT)) != lane;
     wave_sync();
-    if (there) mine[pick] = d;
-    wave_sync();
-    if (__ballot(shared) != 0) {
-        if (there) mine[pick] = 0.0f;
+    if (__ballot(shared) == 0) {
+        if (there) mine[pick] = d;
+    } else {
+        if (there) claim(0.0f);
         wave_sync();
 #pragma unroll 1
         for (int n = 0; n < a.k; ++n) {
@@ -474,6 +475,7 @@ __global__ __launch_bounds__(256) void route_topk_bwd_kernel(RouteArgs a) {
             wave_sync();
         }
     }
+    wave_sync();
     const float share = DENSE && all_sum > 0.0f ? q / all_sum : 0.0f;
     T* dx = static_cast<T*>(a.dlogits) + r * a.ldd;
 #pragma unroll

@@ -352,7 +352,8 @@ __device__ __forceinline__ int w4_pairs(const W4Experts& a, int id, int first, i
 }
 
 // L1: NT / 2 tiles of gate columns and as many of the up columns of the same intermediate columns;
-// act[pair] = silu(gate) up, formed in fp32 and rounded to T, the matrix instruction's operand type, in expand8's order.  L2: NT tiles of output columns; stage[pair] = w o in fp32.
+// act[pair] = silu(gate) up, formed in fp32 and rounded to T, the matrix instruction's operand type, in expand8's
+// order.  L2: NT tiles of output columns; stage[pair] = w o in fp32.
 template <typename T, bool L1, int NT, int FLUSH, bool ZEROS, int TEAMS, int KS>
 __global__ __launch_bounds__(64 * TEAMS * KS, 2) void w4_experts_kernel(W4Experts a) {
     extern __shared__ __align__(16) unsigned char lds_raw[];
