@@ -478,6 +478,53 @@ int32_t moe_forward_w4(const moe_shape* shape, int32_t dtype, int32_t group, con
                        const float* topk_w, const uint8_t* w1, const void* s1, const uint8_t* z1, const uint8_t* w2,
                        const void* s2, const uint8_t* z2, void* ws, size_t ws_bytes, void* y, void* stream);
 
+/*
+ * The dense operators of a block around the expert layer: the linear map (the router's gate product,
+ * shared experts, projections), the block norm between two blocks, and the expert layer on packed bf16
+ * weights for the few tokens of a decode step.
+ */
+typedef enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_SILU = 3, MOE_ACT_SWIGLU = 4 } moe_act;
+
+/* Bytes of ws for moe_linear_forward (backward = 0) or moe_linear_backward (1); a pure function, 0 for invalid
+ * sizes. */
+size_t moe_linear_workspace_bytes(int32_t act, int32_t M, int32_t N, int32_t K, int32_t backward);
+
+/*
+ * Linear map with bias, activation and residual:  z = x W + bias,  y = act(z) + residual.
+ *   act: none; relu; gelu, z P(Z <= z) of the normal distribution; silu, z / (1 + exp(-z)); swiglu, where W has the
+ *   columns [gate | up] and act(z) = silu(gate) up.  W has N columns, 2N for swiglu, called C here.
+ *   x        [device] dtype [M, K] (MOE_BF16 or MOE_FP16), leading dimension ldx
+ *   w        [device] dtype, w_by_column 0: [K, C], else [C, K] (a column of W contiguous), leading dimension ldw
+ *   bias     [device] bdtype [C] (dtype or MOE_FP32), may be NULL
+ *   residual [device] odtype [M, N] (ldr), may be NULL; it may be y itself, with ldr = ldy
+ *   y        [device] odtype [M, N] (ldy), odtype dtype or MOE_FP32
+ *   z        [device] dtype [M, C] (ldz), kept for the backward; may be NULL
+ * Products of 16-bit values summed in fp32, everything up to y in fp32; y and z are rounded once.  A split
+ * reduction is added in a fixed order: the same bits on every run.
+ * M 0 .. 2^24 (0: nothing is done), N 1 .. 2^20, K 1 .. 2^20, and at most 2^23 tiles of 128 x 128 in any product
+ * (M x C; in the backward also M x K and K x C).  Pointers need their element's alignment only; with 16-byte
+ * alignment, and sizes and leading dimensions that are multiples of 8, the large products run on a faster path.
+ * y and z must not overlap x, w, each other or (but for y = residual) the residual.  ws [device] 256-B aligned
+ * scratch, which calls in flight at the same time (and graphs replayed at the same time) must not share.
+ */
+int32_t moe_linear_forward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_t act, int32_t M, int32_t N, int32_t K,
+                           const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t w_by_column, const void* bias,
+                           const void* residual, int64_t ldr, void* y, int64_t ldy, void* z, int64_t ldz, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * Backward of moe_linear_forward, from dy [device] odtype [M, N] (lddy) and the z that it kept (not read for
+ * MOE_ACT_NONE): dz = dy act'(z), formed in fp32 and rounded to dtype for the products (relu's slope at 0 is 0), and
+ *   dx = dz W^T   dtype [M, K] (lddx)       dw = x^T dz   dtype, laid out as w (lddw)
+ *   dbias = the sum over the rows of dz before that rounding   bdtype [C]
+ * each of which may be NULL, not all.  The residual's gradient is dy.  M = 0 writes zeros to dw and dbias.
+ * x is read for dw only, w for dx only.
+ */
+int32_t moe_linear_backward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_t act, int32_t M, int32_t N, int32_t K,
+                            const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                            int32_t w_by_column, const void* z, int64_t ldz, void* dx, int64_t lddx, void* dw, int64_t lddw,
+                            void* dbias, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,70 @@
+"""Argument checks of the dense operators of a block (linear map) that need no GPU: every refusal comes back as a
+status before any device work, and the workspace functions are pure functions of the sizes."""
+import pytest
+import torch
+
+import token_dispatch_grouped_route_amd as moe
+
+NULL, SHAPE, WORKSPACE, ALIGN, DEVICE = -1, -2, -4, -5, -7
+A, B, C, D, E = 0x10000, 0x20000, 0x30000, 0x40000, 0x50000   # addresses that no check reads through
+
+
+def linear(dtype=0, bdtype=0, odtype=0, act=0, M=4, N=32, K=64, x=A, ldx=64, w=B, ldw=32, by_column=0, bias=C, res=C, ldr=32, y=D, ldy=32, z=E, ldz=32, ws=A, n=1 << 30):
+    return moe.lib().moe_linear_forward(dtype, bdtype, odtype, act, M, N, K, x, ldx, w, ldw, by_column, bias, res, ldr, y, ldy, z, ldz, ws, n, None)
+
+
+def linear_bwd(dtype=0, bdtype=0, odtype=0, act=3, M=4, N=32, K=64, dy=A, lddy=32, x=A, ldx=64, w=B, ldw=32, by_column=0, z=C, ldz=32, dx=D, lddx=64, dw=E, lddw=32,
+               db=D + 4096, ws=A, n=1 << 30):
+    return moe.lib().moe_linear_backward(dtype, bdtype, odtype, act, M, N, K, dy, lddy, x, ldx, w, ldw, by_column, z, ldz, dx, lddx, dw, lddw, db, ws, n, None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(dtype=2), SHAPE), (dict(dtype=1), SHAPE), (dict(odtype=1), SHAPE), (dict(bdtype=3), SHAPE), (dict(act=5), SHAPE), (dict(act=-1), SHAPE), (dict(M=-1), SHAPE),
+    (dict(M=(1 << 24) + 1), SHAPE), (dict(N=0), SHAPE), (dict(N=(1 << 20) + 1, ldw=1 << 21, ldy=1 << 21, ldr=1 << 21, ldz=1 << 21), SHAPE), (dict(K=0), SHAPE),
+    (dict(M=1 << 24, N=1 << 20, ldw=1 << 20, ldy=1 << 20, ldr=1 << 20, ldz=1 << 20), SHAPE), (dict(ldx=63), SHAPE), (dict(ldw=31), SHAPE), (dict(by_column=1), SHAPE),
+    (dict(ldy=31), SHAPE), (dict(ldr=31), SHAPE), (dict(ldz=31), SHAPE), (dict(act=4, ldw=64), SHAPE), (dict(x=None), NULL), (dict(w=None), NULL), (dict(y=None), NULL),
+    (dict(ws=None), NULL), (dict(y=A), SHAPE), (dict(y=B), SHAPE), (dict(z=A), SHAPE), (dict(z=D), SHAPE), (dict(z=C), SHAPE), (dict(res=D, ldr=40), SHAPE), (dict(x=A + 1), ALIGN),
+    (dict(w=B + 1), ALIGN), (dict(bias=C + 1), ALIGN), (dict(bdtype=2, bias=C + 2), ALIGN), (dict(odtype=2, y=D + 2), ALIGN), (dict(odtype=2, res=C + 2), ALIGN), (dict(ws=A + 64), ALIGN), (dict(n=8), WORKSPACE),
+])
+def test_linear_refusals(bad, status):
+    assert linear(**bad) == status
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(dtype=2), SHAPE), (dict(act=5), SHAPE), (dict(lddy=31), SHAPE), (dict(ldx=63), SHAPE), (dict(ldw=31), SHAPE), (dict(lddw=31), SHAPE), (dict(lddx=63), SHAPE), (dict(ldz=31), SHAPE),
+    (dict(dx=None, dw=None, db=None), NULL), (dict(dy=None), NULL), (dict(x=None), NULL), (dict(w=None), NULL), (dict(z=None), NULL), (dict(ws=None), NULL),
+    (dict(dx=A), SHAPE), (dict(dw=B), SHAPE), (dict(dx=C), SHAPE), (dict(db=B), SHAPE), (dict(dx=D + 1), ALIGN), (dict(dw=E + 1), ALIGN), (dict(z=C + 1), ALIGN), (dict(ws=A + 8), ALIGN), (dict(n=8), WORKSPACE),
+    (dict(M=1 << 24, K=1 << 20, ldx=1 << 20, lddx=1 << 20), SHAPE),
+])
+def test_linear_backward_refusals(bad, status):
+    assert linear_bwd(**bad) == status
+
+
+def test_linear_without_rows():
+    assert linear(M=0, x=None, y=None, ws=None) == 0
+    assert linear_bwd(M=0, dw=None, db=None, dy=None, x=None, ws=None) == 0
+
+
+def test_linear_workspace():
+    f = moe.lib().moe_linear_workspace_bytes
+    for bad in ((5, 4, 32, 64), (0, -1, 32, 64), (0, 4, 0, 64), (0, 4, 32, 0), (0, 1 << 24, 1 << 20, 64)):
+        assert f(*bad, 0) == 0 and f(*bad, 1) == 0
+    for M, N, K in ((0, 32, 64), (1, 4096, 7168), (48, 7168, 2048), (8192, 4096, 7168), (1003, 1407, 2049), (1 << 24, 128, 128)):
+        for act, C in ((0, N), (4, 2 * N)):
+            assert f(act, M, N, K, 0) % 256 == 0 and f(act, M, N, K, 0) > 0
+            assert f(act, M, N, K, 1) >= 2 * M * C
+    with pytest.raises(moe.MoeError):
+        moe.linear_workspace_bytes(4, 0, 64)
+
+
+def test_binding_refuses_host_tensors():
+    x = torch.ones(2, 64, dtype=torch.bfloat16)
+    for call in (lambda: moe.linear(x, x.t()), lambda: moe.linear_forward(x, x.t()), lambda: moe.linear_backward(x, x, x.t()), lambda: moe.linear_forward(None, x)):
+        with pytest.raises(moe.MoeError):
+            call()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not real")
+def test_without_a_gpu_valid_calls_report_the_device():
+    assert linear() == DEVICE and linear_bwd() == DEVICE
+    assert linear(res=D) == DEVICE and linear(by_column=1, ldw=64) == DEVICE and linear(act=4, ldw=64, ldz=64) == DEVICE

@@ -32,6 +32,7 @@ ENTRY_POINTS = (
     "moe_mx_gemm2_combine", "moe_forward_noalloc",
     "moe_norm_forward", "moe_norm_workspace_bytes", "moe_norm_backward", "moe_route_topk",
     "moe_route_topk_backward", "moe_w4_quantize", "moe_w4_linear", "moe_w4_workspace_bytes", "moe_forward_w4",
+    "moe_linear_workspace_bytes", "moe_linear_forward", "moe_linear_backward",
 )
 NOALLOC_SCRATCH_BYTES = 256 * 1024 * 1024   # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 
@@ -101,6 +102,9 @@ def lib():
         L.moe_w4_linear.argtypes = [i32, i32, i32, i32, i32, P, i64, P, P, P, P, i64, P]
         L.moe_w4_workspace_bytes.argtypes = [S]
         L.moe_forward_w4.argtypes = [S, i32, i32] + [P] * 10 + [size, P, P]
+        L.moe_linear_workspace_bytes.argtypes = [i32] * 5
+        L.moe_linear_forward.argtypes = [i32] * 7 + [P, i64, P, i64, i32, P, P, i64, P, i64, P, i64, P, size, P]
+        L.moe_linear_backward.argtypes = [i32] * 7 + [P, i64, P, i64, P, i64, i32, P, i64, P, i64, P, i64, P, P, size, P]
         for n in ENTRY_POINTS[2:]:
             getattr(L, n).restype = size if n.endswith("workspace_bytes") else i32
         _lib = L
@@ -761,3 +765,139 @@ def forward_w4(shape, x, topk_idx, topk_w, w1, w2, ws, y=None, stream=None):
                                     _like(topk_idx, torch.int32, "topk_idx", (T, shape.k), dev), _like(topk_w, torch.float32, "topk_w", (T, shape.k), dev),
                                     *one[:3], *two[:3], p, n, _like(y, x.dtype, "y", (T, H), dev), _handle(dev)), "moe_forward_w4")
     return y
+
+
+# ------------------------------------------------------------------------------------------------
+# Dense operators of a block around the expert layer
+# ------------------------------------------------------------------------------------------------
+_ACT = {None: 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
+
+
+def _matrix(w, name, like):
+    """(address, leading dimension, by column) of a 2-D weight on like's GPU in like's dtype, whose rows or
+    columns are contiguous and do not overlap."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.dtype != like.dtype or w.get_device() != like.get_device():
+        raise MoeError("%s must be a matrix in %s on %s" % (name, like.dtype, like.device))
+    for by_column in (False, True):
+        t = w.t() if by_column else w
+        rows, cols = t.shape
+        if (cols == 1 or t.stride(1) == 1) and (rows == 1 or t.stride(0) >= cols):
+            return t.data_ptr(), t.stride(0) if rows > 1 else cols, by_column
+    raise MoeError("%s must have contiguous rows or columns that do not overlap" % name)
+
+
+def _address(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _scratch(nbytes, like, ws=None):
+    """A workspace of nbytes on like's GPU, or the caller's, checked."""
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if not isinstance(ws, torch.Tensor) or ws.device != like.device or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
+        raise MoeError("ws must be a contiguous tensor of at least %d bytes on %s" % (nbytes, like.device))
+    return ws
+
+
+def linear_workspace_bytes(M, N, K, act=None, backward=False) -> int:
+    n = int(lib().moe_linear_workspace_bytes(_code(_ACT, act, "act"), M, N, K, bool(backward)))
+    if n == 0:
+        raise MoeError("invalid sizes M = %d, N = %d, K = %d for the linear map" % (M, N, K))
+    return n
+
+
+def linear_forward(x, w, bias=None, act=None, residual=None, out_dtype=None, y=None, keep=False, ws=None, stream=None):
+    """(y, z) of y [..., N] = act(z) + residual with z = x [..., K] @ w + bias (moe_linear_forward).  x and w bf16
+    or fp16; w is [K, C], row-major or a transposed view of [C, K] rows; act None, "relu", "gelu", "silu" or "swiglu"
+    (w's columns are [gate | up], N = C / 2; otherwise N = C).  bias [C] in x's dtype or fp32; residual like y, whose dtype
+    is out_dtype, x's or fp32; y may be the residual.  z [..., C] is kept for linear_backward where asked for (None
+    without an activation, whose backward needs none).  ws: linear_workspace_bytes(...) bytes, made if not given."""
+    with _place(x, "x", stream):
+        dev = x.get_device()
+        px, ldx, M, K = _rows(x, "x")
+        pw, ldw, by_column = _matrix(w, "w", x)
+        code = _code(_ACT, act, "act")
+        C = w.shape[1]
+        if w.shape[0] != K or (act == "swiglu" and C % 2 != 0):
+            raise MoeError("w has the shape %s; [%d, %s] is needed" % (tuple(w.shape), K, "2N" if act == "swiglu" else "N"))
+        N = C // 2 if act == "swiglu" else C
+        bd = bias.dtype if bias is not None else x.dtype
+        out = y.dtype if y is not None and out_dtype is None else out_dtype or x.dtype
+        shape = x.shape[:-1] + (N,)
+        if y is None:
+            y = torch.empty(shape, dtype=out, device=x.device)
+        elif y.dtype != out:
+            raise MoeError("y is %s, out_dtype %s" % (y.dtype, out))
+        py, ldy = _rows(y, "y", y, shape)[:2]
+        if y.device != x.device:
+            raise MoeError("y is on %s, x on %s" % (y.device, x.device))
+        pr, ldr = _rows(residual, "residual", y, shape)[:2] if residual is not None else (None, N)
+        z = torch.empty(x.shape[:-1] + (C,), dtype=x.dtype, device=x.device) if keep and act is not None else None
+        nbytes = linear_workspace_bytes(M, N, K, act)
+        ws = _scratch(nbytes, x, ws)
+        _check(lib().moe_linear_forward(_code(_DTYPE, x.dtype, "x.dtype"), _code(_DTYPE, bd, "bias.dtype"), _code(_DTYPE, out, "out_dtype"), code, M, N, K,
+                                        px, ldx, pw, ldw, by_column, _like(bias, bd, "bias", (C,), dev), pr, ldr, py, ldy, _address(z), C,
+                                        ws.data_ptr(), nbytes, _handle(dev)), "moe_linear_forward")
+    return y, z
+
+
+def linear_backward(dy, x, w, z=None, act=None, bias=False, dx=True, dw=True, ws=None, stream=None):
+    """(dx, dw, dbias) of linear_forward (moe_linear_backward), from the z that it kept.  dx, dw and bias (for dbias)
+    say which are wanted; the others are None.  dw has w's dtype and layout; dbias x's dtype, or the one that bias
+    names (x's or fp32)."""
+    with _place(x, "x", stream):
+        dev = x.get_device()
+        px, ldx, M, K = _rows(x, "x")
+        pw, ldw, by_column = _matrix(w, "w", x)
+        code = _code(_ACT, act, "act")
+        C = w.shape[1]
+        if w.shape[0] != K or (act == "swiglu" and C % 2 != 0):
+            raise MoeError("w has the shape %s; [%d, %s] is needed" % (tuple(w.shape), K, "2N" if act == "swiglu" else "N"))
+        N = C // 2 if act == "swiglu" else C
+        if not isinstance(dy, torch.Tensor) or dy.device != x.device:
+            raise MoeError("dy must be a tensor on %s" % x.device)
+        pdy, lddy = _rows(dy, "dy", dy, x.shape[:-1] + (N,))[:2]
+        if act is not None and z is None:
+            raise MoeError("the backward of %s needs the z that the forward kept" % act)
+        pz, ldz = _rows(z, "z", x, x.shape[:-1] + (C,))[:2] if act is not None else (None, C)
+        bd = bias if isinstance(bias, torch.dtype) else x.dtype
+        gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx else None
+        gw = (torch.empty(C, K, dtype=x.dtype, device=x.device).t() if by_column else torch.empty(K, C, dtype=x.dtype, device=x.device)) if dw else None
+        gb = torch.empty(C, dtype=bd, device=x.device) if bias else None
+        if gx is None and gw is None and gb is None:
+            return None, None, None
+        nbytes = linear_workspace_bytes(M, N, K, act, True)
+        ws = _scratch(nbytes, x, ws)
+        _check(lib().moe_linear_backward(_code(_DTYPE, x.dtype, "x.dtype"), _code(_DTYPE, bd, "bias"), _code(_DTYPE, dy.dtype, "dy.dtype"), code, M, N, K,
+                                         pdy, lddy, px, ldx, pw, ldw, by_column, pz, ldz, _address(gx), K, _address(gw), K if by_column else C,
+                                         _address(gb), ws.data_ptr(), nbytes, _handle(dev)), "moe_linear_backward")
+    return gx, gw, gb
+
+
+class _Linear(torch.autograd.Function):
+    """linear_forward, with linear_backward for the gradients of x, w and bias; the residual's is dy."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, act, out_dtype):
+        want = ctx.needs_input_grad
+        y, z = linear_forward(x, w, bias, act, residual, out_dtype, keep=want[0] or want[1] or want[2])
+        ctx.save_for_backward(x, w, z)
+        ctx.act, ctx.bias_dtype = act, bias.dtype if bias is not None else None
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, w, z = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        gx, gw, gb = (None, None, None)
+        if want[0] or want[1] or want[2]:
+            gx, gw, gb = linear_backward(_row_major(dy), x, w, z, ctx.act, want[2] and ctx.bias_dtype, want[0], want[1])
+        return gx, gw, gb, dy if want[3] else None, None, None
+
+
+def linear(x, w, bias=None, act=None, residual=None, out_dtype=None):
+    """act(x @ w + bias) + residual, differentiable in x, w, bias and residual; arguments as for linear_forward.
+    linear(h, gate, out_dtype=torch.float32) makes a router's logits, linear(h, w1, act="swiglu") and
+    linear(a, w2, residual=y) are a shared expert."""
+    return _Linear.apply(x, w, bias, residual, act, out_dtype)

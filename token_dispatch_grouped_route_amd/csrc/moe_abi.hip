@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "moe_internal.h"
+#include "moe_linear.h"
 
 using namespace moe;
 
@@ -672,6 +673,116 @@ int32_t moe_forward_w4(const moe_shape* shape, int32_t dtype, int32_t group, con
     a.w1 = w1, a.s1 = s1, a.z1 = z1, a.w2 = w2, a.s2 = s2, a.z2 = z2;
     a.act = ws, a.stage = reinterpret_cast<float*>(static_cast<char*>(ws) + stage), a.y = y;
     return launched(launch_w4_forward(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------------------------
+// Dense operators of a block: linear map
+// ---------------------------------------------------------------------------------------------
+namespace {
+constexpr int64_t kLinearMaxTiles = 1 << 23;   // of 128 x 128, 256 threads each: grids stay below 2^32 threads
+int64_t tiles128(int64_t m, int64_t n) { return (m + 127) / 128 * ((n + 127) / 128); }
+struct LinearSizes {
+    int64_t M, N, K, C;   // C: columns of the weight and of z
+    bool ok;
+};
+LinearSizes linear_sizes(int32_t act, int32_t M, int32_t N, int32_t K, bool backward) {
+    LinearSizes s{M, N, K, act == MOE_ACT_SWIGLU ? 2 * static_cast<int64_t>(N) : N, false};
+    if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU || M < 0 || M > (1 << 24) || N < 1 || N > (1 << 20) || K < 1 || K > (1 << 20)) return s;
+    s.ok = tiles128(s.M, s.C) <= kLinearMaxTiles && (!backward || (tiles128(s.M, s.K) <= kLinearMaxTiles && tiles128(s.K, s.C) <= kLinearMaxTiles));
+    return s;
+}
+int64_t dz_row(int64_t C) { return (C + 7) / 8 * 8; }
+// The backward's workspace: dz, then the partial rows of db, then the products' partial sums.
+size_t dz_bytes(const LinearSizes& s) { return align_up(static_cast<size_t>(s.M) * dz_row(s.C) * 2); }
+size_t db_bytes(const LinearSizes& s) { return align_up(static_cast<size_t>(slope_slots(s.M, s.N)) * s.C * 4); }
+size_t larger(size_t a, size_t b) { return a > b ? a : b; }
+}  // namespace
+
+size_t moe_linear_workspace_bytes(int32_t act, int32_t M, int32_t N, int32_t K, int32_t backward) {
+    const LinearSizes s = linear_sizes(act, M, N, K, backward != 0);
+    if (!s.ok) return 0;
+    if (!backward) return align_up(product_part_bytes(s.M, s.C, s.K)) + kWsAlign;
+    return dz_bytes(s) + db_bytes(s) + align_up(larger(product_part_bytes(s.M, s.K, s.C), product_part_bytes(s.K, s.C, s.M))) + kWsAlign;
+}
+
+int32_t moe_linear_forward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_t act, int32_t M, int32_t N, int32_t K,
+                           const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t w_by_column, const void* bias,
+                           const void* residual, int64_t ldr, void* y, int64_t ldy, void* z, int64_t ldz, void* ws,
+                           size_t ws_bytes, void* stream) {
+    const LinearSizes s = linear_sizes(act, M, N, K, false);
+    if (!s.ok || !is_16bit(dtype) || (bdtype != dtype && bdtype != MOE_FP32) || (odtype != dtype && odtype != MOE_FP32)) return MOE_ERR_SHAPE;
+    if (bad_ld(ldx, M, K) || bad_ld(ldw, w_by_column ? s.C : K, w_by_column ? K : s.C) || bad_ld(ldy, M, N) || (residual && bad_ld(ldr, M, N)) ||
+        (z && bad_ld(ldz, M, s.C)))
+        return MOE_ERR_SHAPE;
+    if (M == 0) return MOE_OK;
+    if (!x || !w || !y || !ws) return MOE_ERR_NULL;
+    if (y == x || y == w || z == x || z == w || z == y || (residual == y && ldr != ldy) || (residual && residual == z)) return MOE_ERR_SHAPE;
+    if (!aligned_to(x, dtype) || !aligned_to(w, dtype) || !aligned_to(bias, bdtype) || !aligned_to(residual, odtype) || !aligned_to(y, odtype) ||
+        !aligned_to(z, dtype) || (reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) != 0)
+        return MOE_ERR_ALIGN;
+    if (ws_bytes < moe_linear_workspace_bytes(act, M, N, K, 0)) return MOE_ERR_WORKSPACE;
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    Product g = {};
+    g.M = M, g.N = static_cast<int32_t>(s.C), g.K = K, g.b_strided = !w_by_column;
+    g.a = static_cast<const uint16_t*>(x), g.lda = ldx, g.b = static_cast<const uint16_t*>(w), g.ldb = ldw;
+    g.act = act, g.out_cols = N, g.bias = bias, g.residual = residual, g.ldr = ldr, g.y = y, g.ldy = ldy, g.z = z, g.ldz = ldz;
+    g.bias_f32 = bdtype == MOE_FP32, g.y_f32 = odtype == MOE_FP32;
+    return launched(launch_product(g, dtype, ws, static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_linear_backward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_t act, int32_t M, int32_t N, int32_t K,
+                            const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                            int32_t w_by_column, const void* z, int64_t ldz, void* dx, int64_t lddx, void* dw, int64_t lddw,
+                            void* dbias, void* ws, size_t ws_bytes, void* stream) {
+    const LinearSizes s = linear_sizes(act, M, N, K, true);
+    if (!s.ok || !is_16bit(dtype) || (bdtype != dtype && bdtype != MOE_FP32) || (odtype != dtype && odtype != MOE_FP32)) return MOE_ERR_SHAPE;
+    const int64_t wr = w_by_column ? s.C : K, wc = w_by_column ? K : s.C;
+    if (bad_ld(lddy, M, N) || (dw && (bad_ld(ldx, M, K) || bad_ld(lddw, wr, wc))) || (dx && (bad_ld(ldw, wr, wc) || bad_ld(lddx, M, K))) ||
+        (act != MOE_ACT_NONE && bad_ld(ldz, M, s.C)))
+        return MOE_ERR_SHAPE;
+    if (!dx && !dw && !dbias) return MOE_ERR_NULL;
+    if (M == 0 && !dw && !dbias) return MOE_OK;
+    if (!ws || (M > 0 && (!dy || (dw && !x) || (dx && !w) || (act != MOE_ACT_NONE && !z)))) return MOE_ERR_NULL;
+    const void* in[4] = {dy, x, w, z};
+    for (const void* p : in)
+        if (p && (p == dx || p == dw || p == dbias)) return MOE_ERR_SHAPE;   // not in place
+    if (!aligned_to(dy, odtype) || !aligned_to(x, dtype) || !aligned_to(w, dtype) || !aligned_to(z, dtype) || !aligned_to(dx, dtype) || !aligned_to(dw, dtype) ||
+        !aligned_to(dbias, bdtype) || (reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) != 0)
+        return MOE_ERR_ALIGN;
+    if (ws_bytes < moe_linear_workspace_bytes(act, M, N, K, 1)) return MOE_ERR_WORKSPACE;
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    char* at = static_cast<char*>(ws);
+    const bool own_dz = (dx || dw) && (act != MOE_ACT_NONE || odtype == MOE_FP32);   // else dy is dz
+    LinearSlope l = {};
+    l.M = M, l.N = N, l.act = act, l.dy = dy, l.lddy = lddy, l.z = z, l.ldz = ldz, l.dy_f32 = odtype == MOE_FP32;
+    l.dz = own_dz ? at : nullptr, l.lddz = dz_row(s.C);
+    if (dbias) l.part = reinterpret_cast<float*>(at + dz_bytes(s));
+    if (own_dz || dbias) {
+        const int32_t e = launched(launch_linear_slope(l, dtype, bdtype, dbias, st));
+        if (e != MOE_OK) return e;
+    }
+    void* part = at + dz_bytes(s) + db_bytes(s);
+    const uint16_t* dz = static_cast<const uint16_t*>(own_dz ? at : dy);
+    const int64_t lddz = own_dz ? l.lddz : lddy;
+    Product g = {};
+    if (dx) {
+        g.M = M, g.N = K, g.K = static_cast<int32_t>(s.C), g.a = dz, g.lda = lddz, g.b = static_cast<const uint16_t*>(w), g.ldb = ldw;
+        g.b_strided = w_by_column != 0, g.out_cols = K, g.y = dx, g.ldy = lddx;
+        const int32_t e = launched(launch_product(g, dtype, part, st));
+        if (e != MOE_OK) return e;
+    }
+    if (dw) {   // by column: the product's transpose, dz^T x
+        const uint16_t* xs = static_cast<const uint16_t*>(x);
+        g = {};
+        g.a_strided = g.b_strided = true, g.K = M, g.y = dw, g.ldy = lddw;
+        g.M = static_cast<int32_t>(wr), g.N = g.out_cols = static_cast<int32_t>(wc);
+        g.a = w_by_column ? dz : xs, g.lda = w_by_column ? lddz : ldx;
+        g.b = w_by_column ? xs : dz, g.ldb = w_by_column ? ldx : lddz;
+        const int32_t e = launched(launch_product(g, dtype, part, st));
+        if (e != MOE_OK) return e;
+    }
+    return MOE_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,299 @@
+// Products of the linear map on the 32 x 32 x 16 MFMA, fp32 accumulators, 16-bit operands in LDS.
+//
+// A workgroup of four waves (2 x 2) makes a TILE x TILE block of C, in 64-deep steps of the reduction from two
+// LDS slots.  An operand whose reduction is contiguous lies in a slot as rows of 64 (128 bytes), its 16-byte
+// chunks XOR-swizzled by row so that a fragment read spreads over the banks, and one ds_read_b128 is a lane's
+// fragment: 8 consecutive k of a row.  One whose reduction is strided (W in x W, and both operands of x^T dz)
+// lies as 64 rows of TILE elements, as it is in memory, chunks swizzled by k, and two transposed reads
+// (ds_read_b64_tr_b16) make the same fragment: no copy of a transposed operand is ever written.
+#include <type_traits>
+
+#include "moe_linear.h"
+
+namespace moe {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(1))) void g_void;
+typedef __attribute__((address_space(3))) void l_void;
+typedef __attribute__((address_space(3))) s16x4 l_s16x4;
+
+template <typename T> __device__ __forceinline__ f32x16 mfma(u32x4_t a, u32x4_t b, f32x16 c);
+template <> __device__ __forceinline__ f32x16 mfma<bf16_t>(u32x4_t a, u32x4_t b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, a), __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
+}
+template <> __device__ __forceinline__ f32x16 mfma<fp16_t>(u32x4_t a, u32x4_t b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h16x8, a), __builtin_bit_cast(h16x8, b), c, 0, 0, 0);
+}
+
+constexpr int kThreads = 256;   // four waves
+
+// One operand of a workgroup's tile: W virtual rows (A) or columns (B) from `first`, `count` of which exist.
+// For swiglu the virtual columns alternate G gate columns and the G up columns of the same outputs, so that a
+// wave holds both halves of its outputs.
+struct Side {
+    const uint16_t* p;
+    int64_t ld;
+    int first, count;   // real index of the first, and of one past the last
+    int g, up;          // G, and the offset of an up column; g = 0: not paired
+    __device__ __forceinline__ int real(int v) const {   // may be >= the bound, which limit() gives
+        return g ? first + v / (2 * g) * g + v % g + (v / g & 1) * up : first + v;
+    }
+    __device__ __forceinline__ int limit(int v) const { return g ? count + (v / g & 1) * up : count; }
+};
+
+// Moves the operand's 64-deep steps into an LDS slot through registers: instruction i of wave w covers the 1 KB
+// at 1024 (w + 4 i), lane l its 16 bytes at 16 l; the swizzle is applied to what the lane fetches.
+template <bool S, int W> struct Loader {
+    static constexpr int NI = W / 32;   // instructions per wave and step
+    Side o;
+    int red, wave, lane;
+    u32x4_t r[NI];
+
+    __device__ __forceinline__ void load(int step) {
+        const bf16_t* p = reinterpret_cast<const bf16_t*>(o.p);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if constexpr (!S) {
+                const int v = 8 * (wave + 4 * i) + (lane >> 3), c = (lane & 7) ^ ((v >> 1) & 7), k = step * kLinearDepth + 8 * c;
+                const int at = o.real(v);
+                r[i] = load_chunk<bf16_t>(p + at * o.ld + k, at < o.limit(v) ? red - k : 0);
+            } else {
+                constexpr int CH = W / 8;   // chunks of a row
+                const int kr = (wave + 4 * i) * (64 / CH) + lane / CH, c = lane % CH ^ ((kr & 3) << 2), k = step * kLinearDepth + kr;
+                const int at = o.real(8 * c);
+                r[i] = load_chunk<bf16_t>(p + k * o.ld + at, k < red ? o.limit(8 * c) - at : 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(char* slot) const {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) *reinterpret_cast<u32x4_t*>(slot + 1024 * (wave + 4 * i) + 16 * lane) = r[i];
+    }
+};
+
+// The MFMA fragments of a wave's 32-wide blocks: lane l holds 8 consecutive k, from 8 (l / 32), of row l % 32.
+template <bool S, int W> struct Fragments {
+    uint32_t at[4];   // contiguous: per 16-deep part of a step; strided: per block
+    __device__ __forceinline__ void setup(int base, int lane) {   // base: first row of the wave's blocks, a multiple of 64
+        if constexpr (!S) {
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb)
+                at[kb] = static_cast<uint32_t>((base + (lane & 31)) * 128 + (((2 * kb + (lane >> 5)) ^ ((lane >> 1) & 7)) << 4));
+        } else {
+            // lane j of a 16-lane group reads 4 consecutive columns 4 (j % 4) of k row j / 4; it receives the four k of column j
+            const int g = lane >> 4, j = lane & 15, k = 8 * (g >> 1) + (j >> 2);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int c = base / 8 + 4 * b + 2 * (g & 1) + ((j & 3) >> 1);
+                at[b] = static_cast<uint32_t>(k * (2 * W) + ((c ^ ((k & 3) << 2)) << 4) + 8 * (j & 1));
+            }
+        }
+    }
+    __device__ __forceinline__ u32x4_t read(const char* __restrict__ slot, int block, int kb) const {
+        if constexpr (!S) {
+            return *reinterpret_cast<const u32x4_t*>(slot + at[kb] + block * 4096);
+        } else {
+            const char* p = slot + at[block] + kb * (16 * 2 * W);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s16x4*)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s16x4*)(p + 4 * 2 * W));
+            const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            return __builtin_bit_cast(u32x4_t, v);
+        }
+    }
+};
+
+template <int TILE> constexpr int lds_slot() { return 2 * TILE * 2 * kLinearDepth; }   // both operands of a step
+template <int TILE> constexpr int lds_bytes() {
+    const int out = 4 * 32 * (TILE / 2 + 4) * 4;   // 32 rows of each wave's block in fp32
+    return 2 * lds_slot<TILE>() > out ? 2 * lds_slot<TILE>() : out;
+}
+
+// Workgroup b runs on XCD b mod 8: each XCD takes a run of tiles, in blocks of eight rows of tiles, so that the
+// tiles that run together on one XCD share the slices of both operands in its L2.
+__device__ __forceinline__ bool tile_of(const Product& g, int tile, int& tm, int& tn, int& split) {
+    const int rows = (g.M + tile - 1) / tile, cols = (g.N + tile - 1) / tile;
+    const int64_t total = static_cast<int64_t>(rows) * cols * g.splits, per = (total + 7) / 8;
+    int64_t t = static_cast<int64_t>(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || t >= total) return false;
+    split = static_cast<int>(t / (static_cast<int64_t>(rows) * cols));
+    t -= static_cast<int64_t>(split) * rows * cols;
+    const int band = static_cast<int>(t / (8 * static_cast<int64_t>(cols))), in = static_cast<int>(t - band * (8 * static_cast<int64_t>(cols)));
+    const int high = min(8, rows - 8 * band);
+    tm = 8 * band + in % high;
+    tn = in / high;
+    return true;
+}
+
+// The wave's blocks on their way out, 32 rows at a time through LDS (region: 32 rows of WIDE + 4 floats), so
+// that every lane ends up with 8 consecutive columns of a row.  For swiglu the first half of the block's columns are
+// the gate's.
+template <typename T, int NB, int MB>
+__device__ __forceinline__ void write_out(const Product& g, float* region, const f32x16 (&acc)[MB][NB], int64_t m0, int n0, int split, int lane) {
+    constexpr int WIDE = 32 * NB, PITCH = WIDE + 4;
+    const bool pair = g.act == MOE_ACT_SWIGLU;
+    const int chunks = pair ? WIDE / 16 : WIDE / 8, n = n0 + 8 * (lane % chunks);   // n: an output column
+#pragma unroll
+    for (int mi = 0; mi < MB; ++mi) {
+        wave_sync();   // the last rows have been read
+#pragma unroll
+        for (int ni = 0; ni < NB; ++ni)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) region[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * PITCH + 32 * ni + (lane & 31)] = acc[mi][ni][r];
+        wave_sync();
+        for (int row = lane / chunks; row < 32; row += 64 / chunks) {
+            const int64_t m = m0 + 32 * mi + row;
+            if (m >= g.M || n >= g.out_cols) continue;
+            const float* p = region + row * PITCH + 8 * (lane % chunks);
+            float v[8], up[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = p[i];
+            if (pair) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) up[i] = p[WIDE / 2 + i];
+            }
+            if (g.part) {
+                float* to = g.part + (static_cast<int64_t>(split) * g.M + m) * g.N + n;
+                store8<T>(to, 0, true, g.out_cols - n, v);
+                if (pair) store8<T>(to, g.out_cols, true, g.out_cols - n, up);
+            } else {
+                linear_out<T>(g, m, n, v, up);
+            }
+        }
+    }
+}
+
+template <typename T, bool AS, bool BS, int TILE>
+__global__ __launch_bounds__(kThreads, 1) void linear_kernel(Product g) {
+    extern __shared__ __align__(16) char lds[];
+    constexpr int NB = TILE / 64, SLOT = lds_slot<TILE>(), HALF = TILE * 2 * kLinearDepth;
+    int tm, tn, split;
+    if (!tile_of(g, TILE, tm, tn, split)) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
+    const bool pair = g.act == MOE_ACT_SWIGLU;
+    Loader<AS, TILE> a;
+    Loader<BS, TILE> b;
+    a.o = Side{g.a, g.lda, tm * TILE, g.M, 0, 0};
+    b.o = pair ? Side{g.b, g.ldb, tn * (TILE / 2), g.out_cols, TILE / 4, g.out_cols} : Side{g.b, g.ldb, tn * TILE, g.N, 0, 0};
+    a.red = b.red = g.K;
+    a.wave = b.wave = wave;
+    a.lane = b.lane = lane;
+    Fragments<AS, TILE> fa;
+    Fragments<BS, TILE> fb;
+    fa.setup(wm * (TILE / 2), lane);
+    fb.setup(wn * (TILE / 2), lane);
+    const int steps = (g.K + kLinearDepth - 1) / kLinearDepth, j0 = split * g.slots, j1 = min(steps, j0 + g.slots);
+
+    f32x16 acc[NB][NB];
+#pragma unroll
+    for (int mi = 0; mi < NB; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < NB; ++ni) acc[mi][ni] = f32x16{};
+    a.load(j0);
+    b.load(j0);
+    a.store(lds);
+    b.store(lds + HALF);
+    for (int j = j0; j < j1; ++j) {
+        char* cur = lds + (j - j0 & 1) * SLOT;
+        char* other = lds + SLOT - (j - j0 & 1) * SLOT;
+        lds_barrier();   // the step's operands are in LDS, and the last step's no longer read
+        if (j + 1 < j1) {
+            a.load(j + 1);
+            b.load(j + 1);
+        }
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+            u32x4_t af[NB], bf[NB];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) af[i] = fa.read(cur, i, kb), bf[i] = fb.read(cur + HALF, i, kb);
+#pragma unroll
+            for (int mi = 0; mi < NB; ++mi)
+#pragma unroll
+                for (int ni = 0; ni < NB; ++ni) acc[mi][ni] = mfma<T>(af[mi], bf[ni], acc[mi][ni]);
+        }
+        if (j + 1 < j1) {
+            a.store(other);
+            b.store(other + HALF);
+        }
+    }
+    lds_barrier();
+    constexpr int REGION = 32 * (32 * NB + 4);
+    write_out<T, NB, NB>(g, reinterpret_cast<float*>(lds) + wave * REGION, acc, static_cast<int64_t>(tm) * TILE + wm * (TILE / 2),
+                         pair ? tn * (TILE / 2) + wn * (TILE / 4) : tn * TILE + wn * (TILE / 2), split, lane);
+}
+
+// Joins the splits: eight columns of y a thread.
+template <typename T> __global__ __launch_bounds__(256) void linear_join_kernel(Product g) {
+    const int chunks = (g.out_cols + 7) / 8;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, m = at / chunks;
+    if (m >= g.M) return;
+    const int n = static_cast<int>(at - m * chunks) * 8, valid = g.out_cols - n;
+    float v[8] = {}, up[8] = {};
+    for (int s = 0; s < g.splits; ++s) {
+        const float* p = g.part + (static_cast<int64_t>(s) * g.M + m) * g.N + n;
+        float f[8];
+        load8<T>(p, 0, true, valid, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += f[i];
+        if (g.act == MOE_ACT_SWIGLU) {
+            load8<T>(p, g.out_cols, true, valid, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) up[i] += f[i];
+        }
+    }
+    linear_out<T>(g, m, n, v, up);
+}
+
+template <typename T, bool AS, bool BS, int TILE> hipError_t run_product(const Product& g, hipStream_t s) {
+    auto* kernel = &linear_kernel<T, AS, BS, TILE>;
+    constexpr int lds = lds_bytes<TILE>();
+    if (lds > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
+    const int64_t total = static_cast<int64_t>((g.M + TILE - 1) / TILE) * ((g.N + TILE - 1) / TILE) * g.splits;
+    kernel<<<static_cast<unsigned>((total + 7) / 8 * 8), kThreads, lds, s>>>(g);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !g.part) return e;
+    const int64_t threads = static_cast<int64_t>(g.M) * ((g.out_cols + 7) / 8);
+    linear_join_kernel<T><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, s>>>(g);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t run_layouts(const Product& g, hipStream_t s) {
+    if (g.a_strided) return run_product<T, true, true, 128>(g, s);
+    if (g.b_strided) return run_product<T, false, true, 128>(g, s);
+    return run_product<T, false, false, 128>(g, s);
+}
+
+}  // namespace
+
+// Splits of the reduction: enough workgroups for two a CU, each with at least 8 steps.
+int product_splits(int64_t M, int64_t N, int64_t K) {
+    const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128), steps = (K + kLinearDepth - 1) / kLinearDepth;
+    int64_t splits = tiles > 0 ? 512 / tiles : 1;
+    if (splits > steps / 8) splits = steps / 8;
+    if (splits < 1) return 1;
+    const int64_t per = (steps + splits - 1) / splits;
+    return static_cast<int>((steps + per - 1) / per);   // none is empty
+}
+
+size_t product_part_bytes(int64_t M, int64_t N, int64_t K) {
+    const int splits = product_splits(M, N, K);
+    return splits > 1 ? static_cast<size_t>(splits) * M * N * 4 : 0;
+}
+
+hipError_t launch_product(Product g, int dtype, void* part, hipStream_t s) {
+    if (g.M <= 0) return hipSuccess;
+    g.splits = product_splits(g.M, g.N, g.K);
+    const int steps = (g.K + kLinearDepth - 1) / kLinearDepth;
+    g.slots = (steps + g.splits - 1) / g.splits;
+    g.part = g.splits > 1 ? static_cast<float*>(part) : nullptr;
+    return dtype == MOE_BF16 ? run_layouts<bf16_t>(g, s) : run_layouts<fp16_t>(g, s);
+}
+
+}  // namespace moe

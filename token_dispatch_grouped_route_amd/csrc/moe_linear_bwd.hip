@@ -1,0 +1,85 @@
+// The linear map's backward around its two products: dz = dy act'(z), rounded to the operands' type since the
+// matrix instruction takes it as a 16-bit operand, and db = the sum of the unrounded dz over the rows.
+// Memory bound: dy and z are read once, dz written once.
+#include "moe_columns.h"
+#include "moe_linear.h"
+
+namespace moe {
+namespace {
+
+// 512 columns of y by a run of rows a workgroup: a lane holds 8 columns, the four waves take every fourth row.
+constexpr int kSlopeColumns = 512;
+
+template <typename T> __global__ __launch_bounds__(256) void linear_slope_kernel(LinearSlope a) {
+    __shared__ __align__(16) float join[4][2 * kSlopeColumns];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = blockIdx.x * kSlopeColumns + 8 * lane, valid = a.N - n;
+    const bool pair = a.act == MOE_ACT_SWIGLU;
+    float sum[8] = {}, sum_up[8] = {};
+    const int64_t per = (a.M + gridDim.y - 1) / gridDim.y, m1 = min(static_cast<int64_t>(a.M), (blockIdx.y + 1) * per);
+    if (valid > 0) {
+        for (int64_t m = blockIdx.y * per + wave; m < m1; m += 4) {
+            float dy[8], z[8];
+            load8<T>(a.dy, m * a.lddy + n, a.dy_f32, valid, dy);
+            if (a.act != MOE_ACT_NONE) load8<T>(a.z, m * a.ldz + n, false, valid, z);
+            if (pair) {
+                float up[8], dup[8];
+                load8<T>(a.z, m * a.ldz + a.N + n, false, valid, up);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dup[i] = dy[i] * z[i] * sigmoid_f32(z[i]);
+                    dy[i] = dy[i] * up[i] * act_slope_f32(MOE_ACT_SILU, z[i]);
+                    sum_up[i] += dup[i];
+                }
+                store8<T>(a.dz, m * a.lddz + a.N + n, false, valid, dup);
+            } else if (a.act != MOE_ACT_NONE) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dy[i] *= act_slope_f32(a.act, z[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += dy[i];
+            if (a.dz) store8<T>(a.dz, m * a.lddz + n, false, valid, dy);
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) join[wave][8 * lane + i] = sum[i], join[wave][kSlopeColumns + 8 * lane + i] = sum_up[i];
+    __syncthreads();
+    const int64_t cols = pair ? 2 * static_cast<int64_t>(a.N) : a.N;
+    for (int c = threadIdx.x; c < (pair ? 2 : 1) * kSlopeColumns; c += 256) {
+        const int at = blockIdx.x * kSlopeColumns + c % kSlopeColumns;
+        if (at < a.N) a.part[blockIdx.y * cols + c / kSlopeColumns * a.N + at] = join[0][c] + join[1][c] + join[2][c] + join[3][c];
+    }
+}
+
+}  // namespace
+
+// Runs of rows: what fills the chip four workgroups a CU, and at least 16 rows each.
+int64_t slope_slots(int64_t M, int64_t N) {
+    const int64_t cap = 1024 / ((N + kSlopeColumns - 1) / kSlopeColumns), want = (M + 15) / 16;
+    const int64_t n = want < cap ? want : cap;
+    return n > 0 ? n : 1;
+}
+
+hipError_t launch_linear_slope(const LinearSlope& a, int dtype, int bdtype, void* db, hipStream_t s) {
+    const int64_t slots = slope_slots(a.M, a.N), cols = (a.N + kSlopeColumns - 1) / kSlopeColumns;
+    if (a.M > 0) {
+        const dim3 grid(static_cast<unsigned>(cols), static_cast<unsigned>(slots));
+        if (dtype == MOE_BF16) linear_slope_kernel<bf16_t><<<grid, 256, 0, s>>>(a);
+        else linear_slope_kernel<fp16_t><<<grid, 256, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (db) {
+        ColumnSums c = {};
+        c.sum[0] = {a.part, db};
+        c.groups[0] = 1;
+        c.slots[0] = a.M > 0 ? slots : 0;
+        c.cols = a.act == MOE_ACT_SWIGLU ? 2 * a.N : a.N;
+        if (bdtype == MOE_FP32) launch_column_sums<float>(c, s);
+        else if (bdtype == MOE_BF16) launch_column_sums<bf16_t>(c, s);
+        else launch_column_sums<fp16_t>(c, s);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace moe
