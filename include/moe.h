@@ -525,6 +525,54 @@ int32_t moe_linear_backward(int32_t dtype, int32_t bdtype, int32_t odtype, int32
                             int32_t w_by_column, const void* z, int64_t ldz, void* dx, int64_t lddx, void* dw, int64_t lddw,
                             void* dbias, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * Block norm: the seam between two blocks in one pass over the residual stream.  Per row, with N the norm of
+ * moe_norm_forward without weight and bias (kind: layer or RMS; statistics fp32; a row whose statistics are not
+ * finite becomes NaN):
+ *   p = N(b) post_weight + post_bias   with MOE_POST_NORM in parts, else p = b
+ *   r = x_scale x + scale gate p
+ *   n = N(r) pre_weight + pre_bias     with MOE_PRE_NORM; formed from r before its rounding
+ *   x, r        [device] sdtype [rows, cols] (ldx, ldr), the residual stream: dtype or MOE_FP32; r may be x itself, with ldr = ldx
+ *   b, n        [device] dtype [rows, cols] (ldb, ldn), the block's output and the next block's input; n only with MOE_PRE_NORM
+ *   the vectors [device] wdtype [cols], dtype or MOE_FP32; each may be NULL (weights 1, biases 0); biases are for layer
+ *               norms only, a norm's vectors only with its part (MOE_ERR_SHAPE)
+ *   gate        [device] wdtype [gate_rows, cols], may be NULL (1, gate_rows 0); gate_rows divides rows: each row of the gate
+ *               is for rows / gate_rows consecutive rows
+ *   statistics  [device] fp32 [rows], written for the backward; each may be NULL; means for layer norm only
+ * rows >= 0 (0: nothing is done), cols 1 .. 32768, eps >= 0 (MOE_ERR_SHAPE otherwise).  Pointers need their element's
+ * alignment only.  r and n must not overlap each other or (but for r = x) an input.
+ */
+enum { MOE_POST_NORM = 1, MOE_PRE_NORM = 2 };
+int32_t moe_block_norm_forward(int32_t kind, int32_t parts, int32_t dtype, int32_t sdtype, int32_t wdtype, int64_t rows, int32_t cols,
+                               const void* x, int64_t ldx, const void* b, int64_t ldb, float x_scale, float scale,
+                               const void* post_weight, const void* post_bias, const void* gate, int64_t gate_rows,
+                               const void* pre_weight, const void* pre_bias, float eps, void* r, int64_t ldr, void* n, int64_t ldn,
+                               float* post_mean, float* post_rstd, float* pre_mean, float* pre_rstd, void* stream);
+
+/* Bytes of ws for moe_block_norm_backward (a pure function; 0 for invalid arguments); gate_rows 0: no gate. */
+size_t moe_block_norm_workspace_bytes(int64_t rows, int32_t cols, int64_t gate_rows);
+
+/*
+ * Backward of moe_block_norm_forward, from dr [device] sdtype and dn [device] dtype [rows, cols] (either may be NULL: 0; not
+ * both), the forward's r, b and statistics.  With N'(g) = rstd (g - [layer: sum g / cols] - N sum (g N) / cols), N from r as
+ * it is stored:
+ *   t  = dr + N'(dn pre_weight)           dx = x_scale t                      sdtype [rows, cols] (lddx)
+ *   dp = scale gate t                     db = N'(dp post_weight), else dp    dtype [rows, cols] (lddb)
+ *   dgate [gate_rows, cols] = sum over its rows of scale t p;  dpost_weight = sum dp N(b);  dpost_bias = sum dp;
+ *   dpre_weight = sum dn N(r);  dpre_bias = sum dn                            wdtype
+ * summed in fp32 in an order that the sizes fix.  Each gradient may be NULL, not all.  r and the pre norm's statistics
+ * are read only with dn; b only with MOE_POST_NORM or for dgate.  rows = 0 writes zeros to the vectors' gradients (gate_rows
+ * then counts the gate's rows alone).  ws [device] 256-B aligned scratch of moe_block_norm_workspace_bytes bytes that no
+ * other call in flight may share.  dx and db must not overlap an input.
+ */
+int32_t moe_block_norm_backward(int32_t kind, int32_t parts, int32_t dtype, int32_t sdtype, int32_t wdtype, int64_t rows, int32_t cols,
+                                const void* dr, int64_t lddr, const void* dn, int64_t lddn, const void* r, int64_t ldr, const void* b,
+                                int64_t ldb, float x_scale, float scale, const void* post_weight, const void* post_bias, const void* gate,
+                                int64_t gate_rows, const void* pre_weight, const float* post_mean, const float* post_rstd,
+                                const float* pre_mean, const float* pre_rstd, void* dx, int64_t lddx, void* db, int64_t lddb, void* dgate,
+                                void* dpost_weight, void* dpost_bias, void* dpre_weight, void* dpre_bias, void* ws, size_t ws_bytes,
+                                void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -68,3 +68,57 @@ def test_binding_refuses_host_tensors():
 def test_without_a_gpu_valid_calls_report_the_device():
     assert linear() == DEVICE and linear_bwd() == DEVICE
     assert linear(res=D) == DEVICE and linear(by_column=1, ldw=64) == DEVICE and linear(act=4, ldw=64, ldz=64) == DEVICE
+
+
+def block(kind=1, parts=3, dtype=0, sdtype=0, wdtype=0, rows=6, cols=64, x=A, ldx=64, b=B, ldb=64, w1=C, c1=None, gate=C, gate_rows=2, w2=C, c2=None, eps=1e-5, r=D, ldr=64, n=E, ldn=64,
+          stats=(None, A, None, A)):
+    return moe.lib().moe_block_norm_forward(kind, parts, dtype, sdtype, wdtype, rows, cols, x, ldx, b, ldb, 1.0, 1.0, w1, c1, gate, gate_rows, w2, c2, eps, r, ldr, n, ldn, *stats, None)
+
+
+def block_bwd(kind=1, parts=3, dtype=0, sdtype=0, wdtype=0, rows=6, cols=64, dr=A, lddr=64, dn=A, lddn=64, r=B, ldr=64, b=B, ldb=64, w1=C, c1=None, gate=C, gate_rows=2, w2=C,
+              stats=(None, A, None, A), dx=D, lddx=64, db=E, lddb=64, vec=(D + 4096, D + 8192, None, E + 4096, None), ws=A, size=1 << 24):
+    return moe.lib().moe_block_norm_backward(kind, parts, dtype, sdtype, wdtype, rows, cols, dr, lddr, dn, lddn, r, ldr, b, ldb, 1.0, 1.0, w1, c1, gate, gate_rows, w2, *stats, dx, lddx, db,
+                                             lddb, *vec, ws, size, None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(kind=2), SHAPE), (dict(parts=4), SHAPE), (dict(dtype=3), SHAPE), (dict(sdtype=1), SHAPE), (dict(wdtype=1), SHAPE), (dict(rows=-1), SHAPE), (dict(cols=0), SHAPE),
+    (dict(cols=32769, ldx=40000, ldb=40000, ldr=40000, ldn=40000), SHAPE), (dict(ldx=63), SHAPE), (dict(ldb=63), SHAPE), (dict(ldr=63), SHAPE), (dict(ldn=63), SHAPE), (dict(eps=-1.0), SHAPE),
+    (dict(eps=float("nan")), SHAPE), (dict(c1=A), SHAPE), (dict(c2=A), SHAPE), (dict(parts=2), SHAPE), (dict(parts=1), SHAPE), (dict(gate_rows=4), SHAPE), (dict(gate_rows=0), SHAPE),
+    (dict(gate=None), SHAPE), (dict(x=None), NULL), (dict(b=None), NULL), (dict(r=None), NULL), (dict(n=None), NULL), (dict(r=B), SHAPE), (dict(n=A), SHAPE), (dict(n=B), SHAPE), (dict(n=D), SHAPE),
+    (dict(r=A, ldr=72), SHAPE), (dict(x=A + 1), ALIGN), (dict(gate=C + 1), ALIGN), (dict(w2=C + 1), ALIGN), (dict(sdtype=2, x=A + 2), ALIGN), (dict(stats=(None, A + 2, None, A)), ALIGN),
+])
+def test_block_norm_refusals(bad, status):
+    assert block(**bad) == status
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(parts=4), SHAPE), (dict(lddr=63), SHAPE), (dict(lddn=63), SHAPE), (dict(ldr=63), SHAPE), (dict(ldb=63), SHAPE), (dict(lddx=63), SHAPE), (dict(lddb=63), SHAPE),
+    (dict(parts=1, w2=None), SHAPE), (dict(parts=2, w1=None), SHAPE), (dict(vec=(D, D, A, None, None)), SHAPE), (dict(gate=None, gate_rows=0), SHAPE),
+    (dict(dx=None, db=None, vec=(None,) * 5), NULL), (dict(dr=None, dn=None), NULL), (dict(r=None), NULL), (dict(b=None), NULL), (dict(stats=(None, None, None, A)), NULL),
+    (dict(stats=(None, A, None, None)), NULL), (dict(kind=0), NULL), (dict(ws=None), NULL), (dict(dx=A), SHAPE), (dict(db=B), SHAPE), (dict(db=D), SHAPE), (dict(ws=A + 64), ALIGN),
+    (dict(dx=D + 1), ALIGN), (dict(vec=(D + 1, None, None, None, None)), ALIGN), (dict(size=64), WORKSPACE),
+])
+def test_block_norm_backward_refusals(bad, status):
+    assert block_bwd(**bad) == status
+
+
+def test_block_norm_without_rows():
+    assert block(rows=0, x=None, b=None, r=None, n=None) == 0
+    assert block_bwd(rows=0, dr=None, dn=None, r=None, b=None, vec=(None,) * 5, ws=None) == 0
+
+
+def test_block_norm_workspace():
+    f = moe.lib().moe_block_norm_workspace_bytes
+    assert f(-1, 64, 0) == 0 and f(6, 0, 0) == 0 and f(6, 32769, 0) == 0 and f(6, 64, 4) == 0 and f(6, 64, -1) == 0
+    for rows in (0, 1, 16, 17, 1003, 8192, 65536, 10 ** 7):
+        for cols in (1, 64, 7168, 32768):
+            for gate in (0, 1, rows):
+                n = f(rows, cols, gate)
+                assert n > 0 and n % 256 == 0 and n >= 16 * rows + 4 * cols * gate * (rows > 0)
+                assert gate or n <= 16 * rows + 4 * 4 * (2100 * max(cols, 512) + 512)   # a bound on the runs that the rows do not move
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not real")
+def test_block_norm_without_a_gpu():
+    assert block() == DEVICE and block_bwd() == DEVICE and block(r=A) == DEVICE

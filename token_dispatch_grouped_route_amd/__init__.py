@@ -33,6 +33,7 @@ ENTRY_POINTS = (
     "moe_norm_forward", "moe_norm_workspace_bytes", "moe_norm_backward", "moe_route_topk",
     "moe_route_topk_backward", "moe_w4_quantize", "moe_w4_linear", "moe_w4_workspace_bytes", "moe_forward_w4",
     "moe_linear_workspace_bytes", "moe_linear_forward", "moe_linear_backward",
+    "moe_block_norm_forward", "moe_block_norm_workspace_bytes", "moe_block_norm_backward",
 )
 NOALLOC_SCRATCH_BYTES = 256 * 1024 * 1024   # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 
@@ -105,6 +106,9 @@ def lib():
         L.moe_linear_workspace_bytes.argtypes = [i32] * 5
         L.moe_linear_forward.argtypes = [i32] * 7 + [P, i64, P, i64, i32, P, P, i64, P, i64, P, i64, P, size, P]
         L.moe_linear_backward.argtypes = [i32] * 7 + [P, i64, P, i64, P, i64, i32, P, i64, P, i64, P, i64, P, P, size, P]
+        L.moe_block_norm_forward.argtypes = [i32] * 5 + [i64, i32, P, i64, P, i64, f32, f32, P, P, P, i64, P, P, f32, P, i64, P, i64, P, P, P, P, P]
+        L.moe_block_norm_workspace_bytes.argtypes = [i64, i32, i64]
+        L.moe_block_norm_backward.argtypes = ([i32] * 5 + [i64, i32] + [P, i64] * 4 + [f32, f32, P, P, P, i64] + [P] * 5 + [P, i64] * 2 + [P] * 6 + [size, P])
         for n in ENTRY_POINTS[2:]:
             getattr(L, n).restype = size if n.endswith("workspace_bytes") else i32
         _lib = L
@@ -901,3 +905,133 @@ def linear(x, w, bias=None, act=None, residual=None, out_dtype=None):
     linear(h, gate, out_dtype=torch.float32) makes a router's logits, linear(h, w1, act="swiglu") and
     linear(a, w2, residual=y) are a shared expert."""
     return _Linear.apply(x, w, bias, residual, act, out_dtype)
+
+
+def _vectors(x, post, gate, pre):
+    """(dtype, gate rows, addresses of post's weight and bias, the gate, pre's weight and bias) of a block norm's
+    vectors on x's GPU, all of one dtype."""
+    dev, cols = x.get_device(), x.shape[-1]
+    five = (post or (None, None)) + ((gate,) if gate is not None else (None,)) + (pre or (None, None))
+    wd = next((t.dtype for t in five if isinstance(t, torch.Tensor)), x.dtype)
+    gate_rows, shape = 0, None
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2):
+            raise MoeError("gate must be [C] or [G, C]")
+        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
+        shape = gate.shape[:-1] + (cols,)
+    names = ("post weight", "post bias", "gate", "pre weight", "pre bias")
+    return wd, gate_rows, [_like(t, wd, n, shape if n == "gate" else (cols,), dev) for n, t in zip(names, five)]
+
+
+def _pair(norm, name):
+    """A norm's (weight, bias) as a pair, or None for no norm."""
+    if norm is None:
+        return None
+    if not isinstance(norm, (tuple, list)) or len(norm) != 2:
+        raise MoeError("%s must be None or a pair (weight or None, bias or None)" % name)
+    return tuple(norm)
+
+
+def block_norm_forward(x, b, kind="rms", post=None, gate=None, pre=None, eps=1e-5, x_scale=1.0, scale=1.0, r=None, n=None, stream=None):
+    """(r, n, stats) of the seam between two blocks (moe_block_norm_forward):
+        r = x_scale x + scale gate norm(b),  n = norm(r)
+    over the last dimension.  x and r, the residual stream, in b's dtype or fp32; b and n bf16, fp16 or fp32.  post (the norm
+    of b) and pre (the norm of r) are None (no norm; n is then None) or a pair (weight or None, bias or None); gate None, [C]
+    or [G, C] with a row for each G-th of the rows; all in b's dtype or all in fp32.  kind "rms" (no biases) or
+    "layer".  stats, for block_norm_backward: (post mean, post rstd, pre mean, pre rstd), None where there is none.  r may be x."""
+    with _place(x, "x", stream):
+        dev = x.get_device()
+        post, pre = _pair(post, "post"), _pair(pre, "pre")
+        px, ldx, rows, cols = _rows(x, "x")
+        if not isinstance(b, torch.Tensor) or b.device != x.device:
+            raise MoeError("b must be a tensor on %s" % x.device)
+        pb, ldb = _rows(b, "b", b, x.shape)[:2]
+        wd, gate_rows, vec = _vectors(b, post, gate, pre)
+        if r is None:
+            r = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        pr, ldr = _rows(r, "r", x, x.shape)[:2]
+        if pre is None:
+            if n is not None:
+                raise MoeError("n is written with a norm of r only")
+            pn, ldn = None, cols
+        else:
+            if n is None:
+                n = torch.empty(b.shape, dtype=b.dtype, device=x.device)
+            pn, ldn = _rows(n, "n", b, b.shape)[:2]
+        stat = lambda wanted: torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if wanted else None
+        layer = kind == "layer"
+        stats = (stat(post and layer), stat(post), stat(pre and layer), stat(pre))
+        _check(lib().moe_block_norm_forward(_code(_KIND, kind, "kind"), bool(post) + 2 * bool(pre), _code(_DTYPE, b.dtype, "b.dtype"), _code(_DTYPE, x.dtype, "x.dtype"),
+                                            _code(_DTYPE, wd, "the vectors' dtype"), rows, cols, px, ldx, pb, ldb, x_scale, scale, *vec[:3], gate_rows, *vec[3:],
+                                            eps, pr, ldr, pn, ldn, *map(_address, stats), _handle(dev)), "moe_block_norm_forward")
+    return r, n, stats
+
+
+_BLOCK_NORM_GRADS = ("x", "b", "gate", "post_weight", "post_bias", "pre_weight", "pre_bias")
+
+
+def block_norm_backward(dr, dn, r, b, stats, kind="rms", post=None, gate=None, pre=None, x_scale=1.0, scale=1.0, want=_BLOCK_NORM_GRADS, stream=None):
+    """(dx, db, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias) of block_norm_forward (moe_block_norm_backward)
+    from the gradients of r and n (either may be None), the forward's r, b and stats.  want names the gradients to
+    make ("x", "b", "gate", "post_weight", ...); the others, and those of what there is not, are None."""
+    with _place(b, "b", stream):
+        dev, wanted = b.get_device(), set(want)
+        post, pre = _pair(post, "post"), _pair(pre, "pre")
+        if not wanted <= set(_BLOCK_NORM_GRADS):
+            raise MoeError("want holds %s; known are %s" % (sorted(wanted), _BLOCK_NORM_GRADS))
+        pb, ldb, rows, cols = _rows(b, "b")
+        if not isinstance(r, torch.Tensor) or r.device != b.device:
+            raise MoeError("r must be a tensor on %s" % b.device)
+        pr, ldr = _rows(r, "r", r, b.shape)[:2]
+        pdr, lddr = _rows(dr, "dr", r, b.shape)[:2] if dr is not None else (None, cols)
+        pdn, lddn = _rows(dn, "dn", b, b.shape)[:2] if dn is not None else (None, cols)
+        wd, gate_rows, vec = _vectors(b, post, gate, pre)
+        stat = [_like(t, torch.float32, "stats", b.shape[:-1], dev) for t in stats]
+        made = {"x": torch.empty(b.shape, dtype=r.dtype, device=b.device) if "x" in wanted else None,
+                "b": torch.empty(b.shape, dtype=b.dtype, device=b.device) if "b" in wanted else None}
+        five = (post or (None, None)) + (gate,) + (pre or (None, None))
+        for name, t in zip(("post_weight", "post_bias", "gate", "pre_weight", "pre_bias"), five):
+            made[name] = torch.empty_like(t) if t is not None and name in wanted else None
+        grads = tuple(made[name] for name in _BLOCK_NORM_GRADS)
+        if all(g is None for g in grads):
+            return grads
+        nbytes = int(lib().moe_block_norm_workspace_bytes(rows, cols, gate_rows))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=b.device)
+        dx, db = grads[:2]
+        _check(lib().moe_block_norm_backward(_code(_KIND, kind, "kind"), bool(post) + 2 * bool(pre), _code(_DTYPE, b.dtype, "b.dtype"), _code(_DTYPE, r.dtype, "r.dtype"),
+                                             _code(_DTYPE, wd, "the vectors' dtype"), rows, cols, pdr, lddr, pdn, lddn, pr, ldr, pb, ldb, x_scale, scale, *vec[:3],
+                                             gate_rows, vec[3], *stat, _address(dx), cols, _address(db), cols, *map(_address, grads[2:]), ws.data_ptr(), nbytes,
+                                             _handle(dev)), "moe_block_norm_backward")
+    return grads
+
+
+class _BlockNorm(torch.autograd.Function):
+    """block_norm_forward, with block_norm_backward for the gradients of x, b and the vectors."""
+
+    @staticmethod
+    def forward(ctx, x, b, gate, post_weight, post_bias, pre_weight, pre_bias, kind, post, pre, eps, x_scale, scale):
+        post, pre = (post_weight, post_bias) if post else None, (pre_weight, pre_bias) if pre else None
+        r, n, stats = block_norm_forward(x, b, kind, post, gate, pre, eps, x_scale, scale)
+        ctx.save_for_backward(r, b, gate, post_weight, post_bias, pre_weight, pre_bias, *stats)
+        ctx.how = kind, post is not None, pre is not None, x_scale, scale
+        ctx.set_materialize_grads(False)
+        return r, n
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dr, dn):
+        r, b, gate, w1, c1, w2, c2, *stats = ctx.saved_tensors
+        kind, post, pre, x_scale, scale = ctx.how
+        if dr is None and dn is None:
+            return (None,) * 13
+        want = [name for name, need in zip(_BLOCK_NORM_GRADS, ctx.needs_input_grad) if need]
+        dr, dn = (_row_major(t) if t is not None else None for t in (dr, dn))
+        grads = block_norm_backward(dr, dn, r, b, stats, kind, (w1, c1) if post else None, gate, (w2, c2) if pre else None, x_scale, scale, want)
+        return grads + (None,) * 6
+
+
+def block_norm(x, b, gate=None, post_weight=None, post_bias=None, pre_weight=None, pre_bias=None, kind="rms", post=True, pre=True, eps=1e-5,
+               x_scale=1.0, scale=1.0):
+    """(r, n): r = x_scale x + scale gate norm(b) and n = norm(r), differentiable in x, b, the gate, weights and biases;
+    post and pre say which of the two norms there is (n is None without pre).  Otherwise as block_norm_forward."""
+    return _BlockNorm.apply(x, b, gate, post_weight, post_bias, pre_weight, pre_bias, kind, post, pre, eps, x_scale, scale)

@@ -5,6 +5,7 @@
 
 #include <mutex>
 
+#include "moe_block_norm.h"
 #include "moe_internal.h"
 #include "moe_linear.h"
 
@@ -783,6 +784,103 @@ int32_t moe_linear_backward(int32_t dtype, int32_t bdtype, int32_t odtype, int32
         if (e != MOE_OK) return e;
     }
     return MOE_OK;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Block norm
+// ---------------------------------------------------------------------------------------------
+namespace {
+// The checks that both directions share; fills the formula's part of `a`.
+int32_t check_block_norm(BlockNorm* a, int32_t kind, int32_t parts, int32_t dtype, int32_t sdtype, int32_t wdtype, int64_t rows, int32_t cols, int64_t ldb,
+                         float x_scale, float scale, const void* post_weight, const void* post_bias, const void* gate, int64_t gate_rows,
+                         const void* pre_weight, const void* pre_bias) {
+    const int32_t st = check_norm(kind, dtype, wdtype, rows, cols);
+    if (st != MOE_OK) return st;
+    if ((sdtype != dtype && sdtype != MOE_FP32) || (parts & ~(MOE_POST_NORM | MOE_PRE_NORM)) != 0) return MOE_ERR_SHAPE;
+    const bool post = (parts & MOE_POST_NORM) != 0, pre = (parts & MOE_PRE_NORM) != 0, layer = kind == MOE_LAYER_NORM;
+    if ((!post && (post_weight || post_bias)) || (!pre && (pre_weight || pre_bias)) || (!layer && (post_bias || pre_bias))) return MOE_ERR_SHAPE;
+    if ((gate != nullptr) != (gate_rows > 0) || gate_rows < 0 || (gate_rows > 0 && rows % gate_rows != 0)) return MOE_ERR_SHAPE;
+    if (!aligned_to(post_weight, wdtype) || !aligned_to(post_bias, wdtype) || !aligned_to(gate, wdtype) || !aligned_to(pre_weight, wdtype) ||
+        !aligned_to(pre_bias, wdtype))
+        return MOE_ERR_ALIGN;
+    *a = {};
+    a->rows = rows, a->cols = cols, a->layer = layer, a->post = post, a->pre = pre, a->x_scale = x_scale, a->scale = scale;
+    a->b_f32 = dtype == MOE_FP32, a->s_f32 = sdtype == MOE_FP32, a->w_f32 = wdtype == MOE_FP32;
+    a->post_weight = post_weight, a->post_bias = post_bias, a->gate = gate, a->pre_weight = pre_weight, a->pre_bias = pre_bias, a->ldb = ldb;
+    a->gate_share = gate_rows > 0 ? rows / gate_rows : rows;
+    return MOE_OK;
+}
+}  // namespace
+
+int32_t moe_block_norm_forward(int32_t kind, int32_t parts, int32_t dtype, int32_t sdtype, int32_t wdtype, int64_t rows, int32_t cols,
+                               const void* x, int64_t ldx, const void* b, int64_t ldb, float x_scale, float scale,
+                               const void* post_weight, const void* post_bias, const void* gate, int64_t gate_rows,
+                               const void* pre_weight, const void* pre_bias, float eps, void* r, int64_t ldr, void* n, int64_t ldn,
+                               float* post_mean, float* post_rstd, float* pre_mean, float* pre_rstd, void* stream) {
+    BlockNorm a;
+    const int32_t st = check_block_norm(&a, kind, parts, dtype, sdtype, wdtype, rows, cols, ldb, x_scale, scale, post_weight, post_bias, gate, gate_rows,
+                                        pre_weight, pre_bias);
+    if (st != MOE_OK) return st;
+    if (!(eps >= 0.0f) || bad_ld(ldx, rows, cols) || bad_ld(ldb, rows, cols) || bad_ld(ldr, rows, cols) || (a.pre ? bad_ld(ldn, rows, cols) : n != nullptr))
+        return MOE_ERR_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (!x || !b || !r || (a.pre && !n)) return MOE_ERR_NULL;
+    if (r == b || n == b || n == x || n == r || (r == x && ldr != ldx)) return MOE_ERR_SHAPE;
+    if (!aligned_to(x, sdtype) || !aligned_to(r, sdtype) || !aligned_to(b, dtype) || !aligned_to(n, dtype) || !aligned4(post_mean) || !aligned4(post_rstd) ||
+        !aligned4(pre_mean) || !aligned4(pre_rstd))
+        return MOE_ERR_ALIGN;
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    a.eps = eps, a.x = x, a.ldx = ldx, a.b = b, a.r = r, a.ldr = ldr, a.n = n, a.ldn = ldn;
+    a.post_mean = post_mean, a.post_rstd = post_rstd, a.pre_mean = pre_mean, a.pre_rstd = pre_rstd;
+    return launched(launch_block_norm_fwd(a, dtype, sdtype, wdtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_block_norm_workspace_bytes(int64_t rows, int32_t cols, int64_t gate_rows) {
+    if (check_norm(MOE_LAYER_NORM, MOE_FP32, MOE_FP32, rows, cols) != MOE_OK || gate_rows < 0 || (gate_rows > 0 && rows % gate_rows != 0)) return 0;
+    return block_norm_bwd_bytes(rows, cols, gate_rows);
+}
+
+int32_t moe_block_norm_backward(int32_t kind, int32_t parts, int32_t dtype, int32_t sdtype, int32_t wdtype, int64_t rows, int32_t cols,
+                                const void* dr, int64_t lddr, const void* dn, int64_t lddn, const void* r, int64_t ldr, const void* b,
+                                int64_t ldb, float x_scale, float scale, const void* post_weight, const void* post_bias, const void* gate,
+                                int64_t gate_rows, const void* pre_weight, const float* post_mean, const float* post_rstd,
+                                const float* pre_mean, const float* pre_rstd, void* dx, int64_t lddx, void* db, int64_t lddb, void* dgate,
+                                void* dpost_weight, void* dpost_bias, void* dpre_weight, void* dpre_bias, void* ws, size_t ws_bytes,
+                                void* stream) {
+    BlockNorm a;
+    const int32_t st = check_block_norm(&a, kind, parts, dtype, sdtype, wdtype, rows, cols, ldb, x_scale, scale, post_weight, post_bias, gate, gate_rows,
+                                        pre_weight, nullptr);
+    if (st != MOE_OK) return st;
+    const bool needs_b = a.post || dgate;
+    if ((dr && bad_ld(lddr, rows, cols)) || (dn && (bad_ld(lddn, rows, cols) || bad_ld(ldr, rows, cols))) || (needs_b && bad_ld(ldb, rows, cols)) ||
+        (dx && bad_ld(lddx, rows, cols)) || (db && bad_ld(lddb, rows, cols)))
+        return MOE_ERR_SHAPE;
+    if ((!a.pre && (dn || dpre_weight || dpre_bias)) || (!a.post && (dpost_weight || dpost_bias)) || (!a.layer && (dpre_bias || dpost_bias)) || (dgate && !gate))
+        return MOE_ERR_SHAPE;
+    const bool vectors = dgate || dpost_weight || dpost_bias || dpre_weight || dpre_bias;
+    if (!dx && !db && !vectors) return MOE_ERR_NULL;
+    if (rows == 0 && !vectors) return MOE_OK;
+    if (!ws || (rows > 0 && ((!dr && !dn) || (dn && (!r || !pre_rstd || (a.layer && !pre_mean))) || (needs_b && !b) ||
+                             (a.post && (!post_rstd || (a.layer && !post_mean))))))
+        return MOE_ERR_NULL;
+    const void* in[4] = {dr, dn, r, b};
+    for (const void* p : in)
+        if (p && (p == dx || p == db)) return MOE_ERR_SHAPE;   // not in place
+    if (dx && dx == db) return MOE_ERR_SHAPE;
+    if (!aligned_to(dr, sdtype) || !aligned_to(dx, sdtype) || !aligned_to(r, sdtype) || !aligned_to(dn, dtype) || !aligned_to(b, dtype) || !aligned_to(db, dtype) ||
+        !aligned_to(dgate, wdtype) || !aligned_to(dpost_weight, wdtype) || !aligned_to(dpost_bias, wdtype) || !aligned_to(dpre_weight, wdtype) ||
+        !aligned_to(dpre_bias, wdtype) || !aligned4(post_mean) || !aligned4(post_rstd) || !aligned4(pre_mean) || !aligned4(pre_rstd) ||
+        (reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) != 0)
+        return MOE_ERR_ALIGN;
+    if (ws_bytes < moe_block_norm_workspace_bytes(rows, cols, gate_rows)) return MOE_ERR_WORKSPACE;
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    if (rows == 0) a.gate_share = gate_rows;
+    a.dr = dr, a.lddr = lddr, a.dn = dn, a.lddn = lddn, a.r = const_cast<void*>(dn ? r : nullptr), a.ldr = ldr, a.b = needs_b ? b : nullptr;
+    a.post_mean = const_cast<float*>(post_mean), a.post_rstd = const_cast<float*>(post_rstd);
+    a.pre_mean = const_cast<float*>(pre_mean), a.pre_rstd = const_cast<float*>(pre_rstd);
+    a.dx = dx, a.lddx = lddx, a.db = db, a.lddb = lddb, a.dgate = dgate, a.dpost_weight = dpost_weight, a.dpost_bias = dpost_bias;
+    a.dpre_weight = dpre_weight, a.dpre_bias = dpre_bias, a.ws = static_cast<float*>(ws);
+    return launched(launch_block_norm_bwd(a, dtype, wdtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
