@@ -573,6 +573,20 @@ int32_t moe_block_norm_backward(int32_t kind, int32_t parts, int32_t dtype, int3
                                 void* dpost_weight, void* dpost_bias, void* dpre_weight, void* dpre_bias, void* ws, size_t ws_bytes,
                                 void* stream);
 
+/* Bytes of ws for moe_forward_few (a pure function; 0 for an invalid shape). */
+size_t moe_few_workspace_bytes(const moe_shape* shape);
+
+/*
+ * Expert layer for the few tokens of a decode step, on the weights that moe_forward takes: y as moe_forward defines
+ * it (SwiGLU rounded to bf16 between L1 and L2, the combine summed in fp32 in slot order, the same bits on every run), without
+ * routing tables and row blocks: an expert's weights are read once per 32 of its pairs, straight into the matrix
+ * instruction.  x, topk_idx, topk_w, w1p, w2p, y as for moe_forward.  T * k at most 4096, H and I at most 32768
+ * (MOE_ERR_SHAPE); shape->train must be 0; block_m is not used.  ws [device] 256-B aligned scratch, which calls in flight
+ * at the same time (and graphs replayed at the same time) must not share.
+ */
+int32_t moe_forward_few(const moe_shape* shape, const uint16_t* x, const int32_t* topk_idx, const float* topk_w, const uint16_t* w1p,
+                        const uint16_t* w2p, void* ws, size_t ws_bytes, uint16_t* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

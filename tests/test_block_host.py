@@ -1,5 +1,7 @@
-"""Argument checks of the dense operators of a block (linear map) that need no GPU: every refusal comes back as a
+"""Argument checks of the dense operators of a block (linear map, block norm, few tokens) that need no GPU: every refusal comes back as a
 status before any device work, and the workspace functions are pure functions of the sizes."""
+import ctypes
+
 import pytest
 import torch
 
@@ -122,3 +124,25 @@ def test_block_norm_workspace():
 @pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not real")
 def test_block_norm_without_a_gpu():
     assert block() == DEVICE and block_bwd() == DEVICE and block(r=A) == DEVICE
+
+
+def few(s, x=A, idx=A, tw=A, w1=B, w2=B, ws=C, n=1 << 30, y=D):
+    return moe.lib().moe_forward_few(ctypes.byref(s) if s is not None else None, x, idx, tw, w1, w2, ws, n, y, None)
+
+
+def test_forward_few_refusals():
+    shape = lambda: moe.make_shape(4, 256, 128, 8, 8, 2, block_m=64)
+    assert few(None) == NULL
+    for bad, status in [(dict(x=None), NULL), (dict(idx=None), NULL), (dict(tw=None), NULL), (dict(w1=None), NULL), (dict(w2=None), NULL), (dict(ws=None), NULL), (dict(y=None), NULL),
+                        (dict(ws=C + 64), ALIGN), (dict(w2=B + 8), ALIGN), (dict(x=A + 2), ALIGN), (dict(idx=A + 2), ALIGN), (dict(y=D + 8), ALIGN), (dict(n=64), WORKSPACE)]:
+        assert few(shape(), **bad) == status, bad
+    for change in (dict(T=2049), dict(train=1), dict(H=100), dict(k=33), dict(EL=0), dict(H=32768 + 128), dict(I=32768 + 128), dict(T=-1), dict(e_lo=1)):
+        t = shape()
+        for f, v in change.items():
+            setattr(t, f, v)
+        assert few(t) == SHAPE and moe.lib().moe_few_workspace_bytes(ctypes.byref(t)) == 0
+    assert moe.few_workspace_bytes(shape()) >= 8 * (128 * 2 + 256 * 4)
+    with pytest.raises(moe.MoeError):
+        moe.few_workspace_bytes(moe.make_shape(2049, 256, 128, 8, 8, 2, block_m=64))
+    if not torch.cuda.is_available():
+        assert few(shape()) == DEVICE

@@ -34,6 +34,7 @@ ENTRY_POINTS = (
     "moe_route_topk_backward", "moe_w4_quantize", "moe_w4_linear", "moe_w4_workspace_bytes", "moe_forward_w4",
     "moe_linear_workspace_bytes", "moe_linear_forward", "moe_linear_backward",
     "moe_block_norm_forward", "moe_block_norm_workspace_bytes", "moe_block_norm_backward",
+    "moe_few_workspace_bytes", "moe_forward_few",
 )
 NOALLOC_SCRATCH_BYTES = 256 * 1024 * 1024   # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 
@@ -109,6 +110,8 @@ def lib():
         L.moe_block_norm_forward.argtypes = [i32] * 5 + [i64, i32, P, i64, P, i64, f32, f32, P, P, P, i64, P, P, f32, P, i64, P, i64, P, P, P, P, P]
         L.moe_block_norm_workspace_bytes.argtypes = [i64, i32, i64]
         L.moe_block_norm_backward.argtypes = ([i32] * 5 + [i64, i32] + [P, i64] * 4 + [f32, f32, P, P, P, i64] + [P] * 5 + [P, i64] * 2 + [P] * 6 + [size, P])
+        L.moe_few_workspace_bytes.argtypes = [S]
+        L.moe_forward_few.argtypes = [S] + [P] * 6 + [size, P, P]
         for n in ENTRY_POINTS[2:]:
             getattr(L, n).restype = size if n.endswith("workspace_bytes") else i32
         _lib = L
@@ -1035,3 +1038,33 @@ def block_norm(x, b, gate=None, post_weight=None, post_bias=None, pre_weight=Non
     """(r, n): r = x_scale x + scale gate norm(b) and n = norm(r), differentiable in x, b, the gate, weights and biases;
     post and pre say which of the two norms there is (n is None without pre).  Otherwise as block_norm_forward."""
     return _BlockNorm.apply(x, b, gate, post_weight, post_bias, pre_weight, pre_bias, kind, post, pre, eps, x_scale, scale)
+
+
+def few_workspace_bytes(shape: Shape) -> int:
+    n = int(lib().moe_few_workspace_bytes(ctypes.byref(shape)))
+    if n == 0:
+        raise MoeError("invalid shape %r for moe_forward_few (T * k at most 4096, no training)" % (shape,))
+    return n
+
+
+def few_alloc_workspace(shape: Shape, device="cuda") -> torch.Tensor:
+    return torch.empty(few_workspace_bytes(shape), dtype=torch.uint8, device=device)
+
+
+def forward_few(shape, x, topk_idx, topk_w, w1p, w2p, ws, y=None, stream=None):
+    """y [T, H] of the expert layer for the few tokens of a decode step (moe_forward_few), on the packed weights that
+    forward takes; ws is few_alloc_workspace(shape)'s."""
+    with _place(x, "x", stream):
+        dev = x.get_device()
+        T, H = shape.T, shape.H
+        if y is None:
+            y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+        p, n = _ws(ws)
+        if ws.device != x.device:
+            raise MoeError("ws is on %s, x on %s" % (ws.device, x.device))
+        sizes = packed_sizes(shape)
+        _check(lib().moe_forward_few(ctypes.byref(shape), _like(x, torch.bfloat16, "x", (T, H), dev), _like(topk_idx, torch.int32, "topk_idx", (T, shape.k), dev),
+                                     _like(topk_w, torch.float32, "topk_w", (T, shape.k), dev), _like(w1p, torch.bfloat16, "w1p", sizes[0], dev),
+                                     _like(w2p, torch.bfloat16, "w2p", sizes[1], dev), p, n, _like(y, torch.bfloat16, "y", (T, H), dev), _handle(dev)),
+               "moe_forward_few")
+    return y

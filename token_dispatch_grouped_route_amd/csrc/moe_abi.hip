@@ -883,4 +883,42 @@ int32_t moe_block_norm_backward(int32_t kind, int32_t parts, int32_t dtype, int3
     return launched(launch_block_norm_bwd(a, dtype, wdtype, static_cast<hipStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------------------------------------
+// Expert layer for few tokens
+// ---------------------------------------------------------------------------------------------
+namespace {
+// Byte offset of the stage rows and the total; false for a bad shape.
+bool few_layout(const moe_shape* s, size_t* stage, size_t* total) {
+    if (check_shape(s) != MOE_OK || s->train || static_cast<int64_t>(s->T) * s->k > kFewMaxPairs || s->H > kFewMaxK || s->I > kFewMaxK) return false;
+    const size_t pairs = static_cast<size_t>(s->T) * s->k;
+    *stage = align_up(pairs * s->I * 2);
+    *total = *stage + align_up(pairs * s->H * 4) + kWsAlign;
+    return true;
+}
+}  // namespace
+
+size_t moe_few_workspace_bytes(const moe_shape* shape) {
+    size_t stage, total;
+    return few_layout(shape, &stage, &total) ? total : 0;
+}
+
+int32_t moe_forward_few(const moe_shape* shape, const uint16_t* x, const int32_t* topk_idx, const float* topk_w, const uint16_t* w1p,
+                        const uint16_t* w2p, void* ws, size_t ws_bytes, uint16_t* y, void* stream) {
+    const int32_t st = check_shape(shape);
+    if (st != MOE_OK) return st;
+    size_t stage, total;
+    if (!few_layout(shape, &stage, &total)) return MOE_ERR_SHAPE;
+    if (!w1p || !w2p || !ws || ((!x || !topk_idx || !topk_w || !y) && shape->T > 0)) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(w1p) || !aligned16(w2p) || !aligned16(y) || !aligned4(topk_idx) || !aligned4(topk_w) ||
+        (reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) != 0)
+        return MOE_ERR_ALIGN;
+    if (ws_bytes < total) return MOE_ERR_WORKSPACE;
+    if (!is_gfx950()) return MOE_ERR_DEVICE;
+    FewExperts a = {};
+    a.T = shape->T, a.H = shape->H, a.I = shape->I, a.e_lo = shape->e_lo, a.EL = shape->EL, a.k = shape->k;
+    a.x = x, a.topk_idx = topk_idx, a.topk_w = topk_w, a.w1 = w1p, a.w2 = w2p, a.y = y;
+    a.act = static_cast<uint16_t*>(ws), a.stage = reinterpret_cast<float*>(static_cast<char*>(ws) + stage);
+    return launched(launch_few(a, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

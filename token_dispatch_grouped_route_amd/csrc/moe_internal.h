@@ -247,6 +247,20 @@ hipError_t launch_w4_forward(const W4Experts& a, int dtype, hipStream_t s);
 hipError_t launch_w4_quantize(int wdtype, int dtype, int E, int K, int N, int group, const void* w, uint8_t* codes, void* scales,
                               uint8_t* zeros, hipStream_t s);
 
+// The expert layer on packed bf16 weights for few tokens (moe_forward_few).
+struct FewExperts {
+    int32_t T, H, I, e_lo, EL, k;
+    const uint16_t* x;
+    const int32_t* topk_idx;
+    const float* topk_w;
+    const uint16_t *w1, *w2;
+    uint16_t* act;   // [T * k, I], one row per pair
+    float* stage;    // [T * k, H] weighted L2 rows
+    uint16_t* y;
+};
+constexpr int kFewMaxPairs = 4096, kFewMaxK = 32768;   // T * k, H and I of moe_forward_few
+hipError_t launch_few(const FewExperts& a, hipStream_t s);
+
 // Compute units of the current device (cached per device).
 int device_cu_count();
 

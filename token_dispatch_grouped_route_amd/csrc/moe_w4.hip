@@ -23,7 +23,7 @@
 // the other steps 4.3, joining and SwiGLU 0.5, and the slowest workgroup ends 2 later.
 #include <type_traits>
 
-#include "moe_vec.h"
+#include "moe_stream.h"
 
 namespace moe {
 
@@ -83,20 +83,6 @@ __device__ __forceinline__ void transpose_groups(u32x4_t& d) {
 
 constexpr int kW4Chunk = 128;   // k per wave and step
 constexpr int kW4Ahead = 2;     // steps in flight per wave
-
-// Weights and x are read through buffers, whose loads return 0 past the end: an offset of kNoRow or
-// kNoK or more (also of both added) lies past every buffer, none of which exceeds 2^30 bytes.
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-constexpr uint32_t kNoRow = 0x80000000u, kNoK = 0x40000000u;
-__device__ __forceinline__ rsrc_t buffer_of(const void* p, int64_t bytes) {   // the same for the whole wave
-    const uint64_t at = reinterpret_cast<uint64_t>(p);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)), hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(static_cast<uint64_t>(hi) << 32 | lo), 0,
-                                             __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(bytes)), 0x00020000);
-}
-__device__ __forceinline__ u32x4_t load16(rsrc_t r, uint32_t at) {
-    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
-}
 
 // Scales and zero points of a workgroup's NT tiles in LDS: a row per weight row, of `stride` elements, an
 // odd multiple of 8, so that the 16 rows a wave reads at once start in different banks.
@@ -327,30 +313,6 @@ __global__ __launch_bounds__(64 * TEAMS * KS, 2) void w4_linear_kernel(W4Linear 
 // for each (on one XCD, as above) the workgroups that share an expert's passes of 16 rows.  A workgroup lists its
 // expert's pairs in ascending order itself (the ids are a few KB), so no table is built beforehand.
 // ---------------------------------------------------------------------------------------------
-// The pairs of expert id, ascending, and their number; 0 if `first` >= 0 and an earlier pair has it.  Every
-// wave writes the whole list (the same values), so none waits for another.
-__device__ __forceinline__ int w4_pairs(const W4Experts& a, int id, int first, int* list) {
-    const int pairs = a.T * a.k, lane = threadIdx.x & 63;
-    int count = 0, earliest = pairs;
-    constexpr int AHEAD = 8;   // loads in flight
-    for (int p0 = 0; p0 < pairs; p0 += 64 * AHEAD) {
-        int ids[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) ids[i] = a.topk_idx[min(p0 + 64 * i + lane, pairs - 1)];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int p = p0 + 64 * i + lane;
-            const bool mine = p < pairs && ids[i] == id;
-            const uint64_t m = __ballot(mine);
-            if (mine) list[count + __popcll(m & ((uint64_t(1) << lane) - 1))] = p;
-            if (m != 0 && count == 0) earliest = p0 + 64 * i + __ffsll(static_cast<unsigned long long>(m)) - 1;
-            count += __popcll(m);
-        }
-    }
-    wave_sync();   // the list is read by other lanes than those that wrote it
-    return earliest < first ? 0 : count;
-}
-
 // L1: NT / 2 tiles of gate columns and as many of the up columns of the same intermediate columns;
 // act[pair] = silu(gate) up, formed in fp32 and rounded to T, the matrix instruction's operand type, in expand8's
 // order.  L2: NT tiles of output columns; stage[pair] = w o in fp32.
@@ -366,7 +328,7 @@ __global__ __launch_bounds__(64 * TEAMS * KS, 2) void w4_experts_kernel(W4Expert
     const uint32_t passes = a.passes, b = blockIdx.x >> 3, pass = b % passes, block = b / passes * 8 + (blockIdx.x & 7);
     const int col0 = (block * TEAMS + team) * OUT, columns = L1 ? a.I : a.H;
     if (e < 0 || e >= a.EL || static_cast<int>(block * TEAMS) * OUT >= columns) return;
-    const int count = w4_pairs(a, id, by_pair ? static_cast<int>(blockIdx.y) : -1, list), m_first = 16 * pass;
+    const int count = expert_pairs(a.topk_idx, pairs, id, by_pair ? static_cast<int>(blockIdx.y) : -1, list), m_first = 16 * pass;
     if (m_first >= count) return;
 
     const int K = L1 ? a.H : a.I, groups = K >> a.gshift, stride = w4_stride(groups);
