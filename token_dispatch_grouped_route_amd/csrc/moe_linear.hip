@@ -11,6 +11,12 @@
 #include "moe_linear.h"
 
 namespace moe {
+
+struct Plan {
+    bool dma;
+    int tile, splits;
+};
+
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -31,6 +37,7 @@ template <> __device__ __forceinline__ f32x16 mfma<fp16_t>(u32x4_t a, u32x4_t b,
 }
 
 constexpr int kThreads = 256;   // four waves
+
 
 // One operand of a workgroup's tile: W virtual rows (A) or columns (B) from `first`, `count` of which exist.
 // For swiglu the virtual columns alternate G gate columns and the G up columns of the same outputs, so that a
@@ -73,6 +80,51 @@ template <bool S, int W> struct Loader {
     __device__ __forceinline__ void store(char* slot) const {
 #pragma unroll
         for (int i = 0; i < NI; ++i) *reinterpret_cast<u32x4_t*>(slot + 1024 * (wave + 4 * i) + 16 * lane) = r[i];
+    }
+};
+
+// The same straight from memory into LDS, without registers, for operands whose 16-byte chunks are aligned and whole:
+// past the last row (column) the last one is read again (its products are not stored), and past the end of the
+// reduction, a chunk of zeros.
+__device__ __align__(16) const uint32_t kZeroChunk[4] = {0, 0, 0, 0};
+
+template <bool S, int W> struct DmaLoader {
+    static constexpr int NI = W / 32;
+    const char* src[NI];   // this lane's 16 bytes of step 0
+    int64_t step_bytes;
+    int k0, red, wave;     // k0: this lane's first k of instruction 0 in a step
+
+    __device__ __forceinline__ void setup(const Side& o, int reduction, int w, int lane) {
+        red = reduction;
+        wave = w;
+        const char* p = reinterpret_cast<const char*>(o.p);
+        step_bytes = S ? 2 * kLinearDepth * o.ld : 2 * kLinearDepth;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if constexpr (!S) {
+                const int v = 8 * (wave + 4 * i) + (lane >> 3), c = (lane & 7) ^ ((v >> 1) & 7);
+                src[i] = p + 2 * (min(o.real(v), o.limit(v) - 1) * o.ld + 8 * c);
+            } else {
+                constexpr int CH = W / 8;
+                const int kr = (wave + 4 * i) * (64 / CH) + lane / CH, c = lane % CH ^ ((kr & 3) << 2);
+                src[i] = p + 2 * (kr * o.ld + min(o.real(8 * c), o.limit(8 * c) - 8));
+            }
+        }
+        // (v >> 1) & 7 and kr & 3 repeat with the instruction: a lane's k of instruction i is k0 (+ 4 i (64 / CH) where strided)
+        k0 = S ? wave * (64 / (W / 8)) + lane / (W / 8) : 8 * ((lane & 7) ^ ((8 * wave + (lane >> 3)) >> 1 & 7));
+    }
+    __device__ __forceinline__ void issue(int step, char* __restrict__ slot, int i) const {
+        __builtin_amdgcn_global_load_lds((g_void*)(src[i] + step * step_bytes), (l_void*)(slot + 1024 * (wave + 4 * i)), 16, 0, 0);
+    }
+    // a step that may reach past the reduction's end
+    __device__ __forceinline__ void issue_last(int step, char* slot) const {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int k = step * kLinearDepth + k0 + (S ? 4 * i * (64 / (W / 8)) : 0);
+            uint64_t p = reinterpret_cast<uint64_t>(k < red ? src[i] + step * step_bytes : reinterpret_cast<const char*>(kZeroChunk));
+            asm("" : "+v"(p));   // a selected address, not two loads under a branch
+            __builtin_amdgcn_global_load_lds((g_void*)p, (l_void*)(slot + 1024 * (wave + 4 * i)), 16, 0, 0);
+        }
     }
 };
 
@@ -226,6 +278,119 @@ __global__ __launch_bounds__(kThreads, 1) void linear_kernel(Product g) {
                          pair ? tn * (TILE / 2) + wn * (TILE / 4) : tn * TILE + wn * (TILE / 2), split, lane);
 }
 
+// The K loop on DMA loads, two slots.  Per step, 16-deep parts 0 .. 3: each part's MFMAs run between the reads of the
+// next part's fragments.  Before part 3, when this step's slot has been read, one barrier (with every load landed):
+// then the next step's part 0 is read from the other slot and the loads of the step after it go into this one, so a
+// load has one step's time to land and nothing waits but the barrier.
+template <typename T, bool AS, bool BS, int TILE> struct DmaLoop {
+    static constexpr int NB = TILE / 64, HALF = TILE * 2 * kLinearDepth, NI = TILE / 32;
+    DmaLoader<AS, TILE> a;
+    DmaLoader<BS, TILE> b;
+    Fragments<AS, TILE> fa;
+    Fragments<BS, TILE> fb;
+
+    __device__ __forceinline__ void fragments(const char* __restrict__ slot, int kb, u32x4_t (&af)[NB], u32x4_t (&bf)[NB]) const {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) af[i] = fa.read(slot, i, kb), bf[i] = fb.read(slot + HALF, i, kb);
+    }
+    static __device__ __forceinline__ void multiply(const u32x4_t (&af)[NB], const u32x4_t (&bf)[NB], f32x16 (&acc)[NB][NB]) {
+#pragma unroll
+        for (int mi = 0; mi < NB; ++mi)
+#pragma unroll
+            for (int ni = 0; ni < NB; ++ni) acc[mi][ni] = mfma<T>(af[mi], bf[ni], acc[mi][ni]);
+    }
+    // order: MFMA, fragment reads, a load, in turn
+    template <int LOADS> static __device__ __forceinline__ void interleave() {
+        constexpr int NM = NB * NB, NR = NB * ((AS ? 2 : 1) + (BS ? 2 : 1));
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+            for (int x = 0; x * NM < NR; ++x)
+                if (x * NM + i < NR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+            for (int x = 0; x * NM < LOADS; ++x)
+                if (x * NM + i < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    static __device__ __forceinline__ void landed() {
+        __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // MAIN: the step two ahead (`ahead`, at most the last) is whole
+    template <bool MAIN> __device__ __forceinline__ void step(int j, int j1, int ahead, char* __restrict__ cur, char* __restrict__ other, u32x4_t (&af)[2][NB], u32x4_t (&bf)[2][NB],
+                                                              f32x16 (&acc)[NB][NB]) const {
+#pragma unroll
+        for (int kb = 0; kb < 3; ++kb) {
+            fragments(cur, kb + 1, af[(kb + 1) & 1], bf[(kb + 1) & 1]);
+            multiply(af[kb & 1], bf[kb & 1], acc);
+            interleave<0>();
+        }
+        landed();
+        if constexpr (MAIN) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) a.issue(ahead, cur, i), b.issue(ahead, cur + HALF, i);
+            fragments(other, 0, af[0], bf[0]);
+            multiply(af[1], bf[1], acc);
+            interleave<2 * NI>();
+        } else {
+            if (j + 2 < j1) {
+                a.issue_last(j + 2, cur);
+                b.issue_last(j + 2, cur + HALF);
+            }
+            multiply(af[1], bf[1], acc);
+            if (j + 1 < j1) fragments(other, 0, af[0], bf[0]);
+        }
+    }
+    __device__ __forceinline__ void run(int j0, int j1, char* __restrict__ s0, char* __restrict__ s1, f32x16 (&acc)[NB][NB]) const {
+        a.issue_last(j0, s0);
+        b.issue_last(j0, s0 + HALF);
+        landed();   // slot 0; its latency is paid once
+        if (j0 + 1 < j1) {
+            a.issue_last(j0 + 1, s1);
+            b.issue_last(j0 + 1, s1 + HALF);
+        }
+        u32x4_t af[2][NB], bf[2][NB];
+        fragments(s0, 0, af[0], bf[0]);
+        // the steps whose successor two ahead is whole or, where all are, does not matter (the last one is read again)
+        const int whole = min(j1, a.red / kLinearDepth), main = whole == j1 ? j1 : whole - 2;
+        int j = j0;
+        for (; j + 1 < main; j += 2) {
+            step<true>(j, j1, min(j + 2, whole - 1), s0, s1, af, bf, acc);
+            step<true>(j + 1, j1, min(j + 3, whole - 1), s1, s0, af, bf, acc);
+        }
+        for (; j < j1; ++j) step<false>(j, j1, 0, (j - j0) & 1 ? s1 : s0, (j - j0) & 1 ? s0 : s1, af, bf, acc);
+    }
+};
+
+template <typename T, bool AS, bool BS, int TILE>
+__global__ __launch_bounds__(kThreads, TILE == 256 ? 1 : 2) void linear_dma_kernel(Product g) {
+    extern __shared__ __align__(16) char lds[];
+    constexpr int NB = TILE / 64;
+    int tm, tn, split;
+    if (!tile_of(g, TILE, tm, tn, split)) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
+    const bool pair = g.act == MOE_ACT_SWIGLU;
+    DmaLoop<T, AS, BS, TILE> loop;
+    loop.a.setup(Side{g.a, g.lda, tm * TILE, g.M, 0, 0}, g.K, wave, lane);
+    loop.b.setup(pair ? Side{g.b, g.ldb, tn * (TILE / 2), g.out_cols, TILE / 4, g.out_cols} : Side{g.b, g.ldb, tn * TILE, g.N, 0, 0}, g.K, wave, lane);
+    loop.fa.setup(wm * (TILE / 2), lane);
+    loop.fb.setup(wn * (TILE / 2), lane);
+    const int steps = (g.K + kLinearDepth - 1) / kLinearDepth, j0 = split * g.slots, j1 = min(steps, j0 + g.slots);
+    f32x16 acc[NB][NB];
+#pragma unroll
+    for (int mi = 0; mi < NB; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < NB; ++ni) acc[mi][ni] = f32x16{};
+    if (j0 < j1) loop.run(j0, j1, lds, lds + lds_slot<TILE>(), acc);
+    DmaLoop<T, AS, BS, TILE>::landed();
+    constexpr int REGION = 32 * (32 * NB + 4);
+    write_out<T, NB, NB>(g, reinterpret_cast<float*>(lds) + wave * REGION, acc, static_cast<int64_t>(tm) * TILE + wm * (TILE / 2),
+                         pair ? tn * (TILE / 2) + wn * (TILE / 4) : tn * TILE + wn * (TILE / 2), split, lane);
+}
+
 // Joins the splits: eight columns of y a thread.
 template <typename T> __global__ __launch_bounds__(256) void linear_join_kernel(Product g) {
     const int chunks = (g.out_cols + 7) / 8;
@@ -248,8 +413,10 @@ template <typename T> __global__ __launch_bounds__(256) void linear_join_kernel(
     linear_out<T>(g, m, n, v, up);
 }
 
-template <typename T, bool AS, bool BS, int TILE> hipError_t run_product(const Product& g, hipStream_t s) {
-    auto* kernel = &linear_kernel<T, AS, BS, TILE>;
+template <typename T, bool AS, bool BS, int TILE, bool DMA> hipError_t run_product(const Product& g, hipStream_t s) {
+    void (*kernel)(Product);
+    if constexpr (DMA) kernel = &linear_dma_kernel<T, AS, BS, TILE>;
+    else kernel = &linear_kernel<T, AS, BS, TILE>;
     constexpr int lds = lds_bytes<TILE>();
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -264,36 +431,51 @@ template <typename T, bool AS, bool BS, int TILE> hipError_t run_product(const P
     return hipGetLastError();
 }
 
-template <typename T> hipError_t run_layouts(const Product& g, hipStream_t s) {
-    if (g.a_strided) return run_product<T, true, true, 128>(g, s);
-    if (g.b_strided) return run_product<T, false, true, 128>(g, s);
-    return run_product<T, false, false, 128>(g, s);
+// Whether an operand's 16-byte chunks are aligned and whole (extent: what it has along its contiguous dimension).
+bool whole_chunks(const void* p, int64_t ld, int64_t extent) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && extent % 8 == 0; }
+
+template <typename T, bool AS, bool BS> hipError_t run_tiles(const Product& g, const Plan& plan, hipStream_t s) {
+    if (plan.dma && plan.tile == 256) return run_product<T, AS, BS, 256, true>(g, s);
+    if (plan.dma) return run_product<T, AS, BS, 128, true>(g, s);
+    return run_product<T, AS, BS, 128, false>(g, s);
+}
+template <typename T> hipError_t run_layouts(const Product& g, const Plan& plan, hipStream_t s) {
+    if (g.a_strided) return run_tiles<T, true, true>(g, plan, s);
+    if (g.b_strided) return run_tiles<T, false, true>(g, plan, s);
+    return run_tiles<T, false, false>(g, plan, s);
 }
 
 }  // namespace
 
-// Splits of the reduction: enough workgroups for two a CU, each with at least 8 steps.
-int product_splits(int64_t M, int64_t N, int64_t K) {
-    const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128), steps = (K + kLinearDepth - 1) / kLinearDepth;
-    int64_t splits = tiles > 0 ? 512 / tiles : 1;
+// Tile and splits of the reduction.
+Plan product_plan(int64_t M, int64_t N, int64_t K, bool dma) {
+    const int64_t steps = (K + kLinearDepth - 1) / kLinearDepth;
+    Plan p{dma, 128, 1};
+    if (M <= 0 || steps == 0) return p;
+    if (dma && ((M + 255) / 256) * ((N + 255) / 256) >= 200) p.tile = 256;
+    const int64_t tiles = (M + p.tile - 1) / p.tile * ((N + p.tile - 1) / p.tile), room = p.tile == 256 ? 256 : 512;
+    int64_t splits = room / tiles;
     if (splits > steps / 8) splits = steps / 8;
-    if (splits < 1) return 1;
+    if (splits < 1) return p;
     const int64_t per = (steps + splits - 1) / splits;
-    return static_cast<int>((steps + per - 1) / per);   // none is empty
+    p.splits = static_cast<int>((steps + per - 1) / per);   // none is empty
+    return p;
 }
 
-size_t product_part_bytes(int64_t M, int64_t N, int64_t K) {
-    const int splits = product_splits(M, N, K);
+size_t product_part_bytes(int64_t M, int64_t N, int64_t K) {   // whatever the alignment
+    const int with = product_plan(M, N, K, true).splits, without = product_plan(M, N, K, false).splits, splits = with > without ? with : without;
     return splits > 1 ? static_cast<size_t>(splits) * M * N * 4 : 0;
 }
 
 hipError_t launch_product(Product g, int dtype, void* part, hipStream_t s) {
     if (g.M <= 0) return hipSuccess;
-    g.splits = product_splits(g.M, g.N, g.K);
+    const bool whole = whole_chunks(g.a, g.lda, g.a_strided ? g.M : g.K) && whole_chunks(g.b, g.ldb, g.b_strided ? (g.act == MOE_ACT_SWIGLU ? g.out_cols : g.N) : g.K);
+    const Plan plan = product_plan(g.M, g.N, g.K, whole);
+    g.splits = plan.splits;
     const int steps = (g.K + kLinearDepth - 1) / kLinearDepth;
     g.slots = (steps + g.splits - 1) / g.splits;
     g.part = g.splits > 1 ? static_cast<float*>(part) : nullptr;
-    return dtype == MOE_BF16 ? run_layouts<bf16_t>(g, s) : run_layouts<fp16_t>(g, s);
+    return dtype == MOE_BF16 ? run_layouts<bf16_t>(g, plan, s) : run_layouts<fp16_t>(g, plan, s);
 }
 
 }  // namespace moe
