@@ -550,7 +550,7 @@ int32_t moe_block_norm_forward(int32_t kind, int32_t parts, int32_t dtype, int32
                                float* post_mean, float* post_rstd, float* pre_mean, float* pre_rstd, void* stream);
 
 /* Bytes of ws for moe_block_norm_backward (a pure function; 0 for invalid arguments); gate_rows 0: no gate. */
-size_t moe_block_norm_workspace_bytes(int64_t rows, int32_t cols, int64_t gate_rows);
+size_t moe_block_norm_workspace_bytes(int32_t dtype, int64_t rows, int32_t cols, int64_t gate_rows);
 
 /*
  * Backward of moe_block_norm_forward, from dr [device] sdtype and dn [device] dtype [rows, cols] (either may be NULL: 0; not

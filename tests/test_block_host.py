@@ -112,13 +112,15 @@ def test_block_norm_without_rows():
 
 def test_block_norm_workspace():
     f = moe.lib().moe_block_norm_workspace_bytes
-    assert f(-1, 64, 0) == 0 and f(6, 0, 0) == 0 and f(6, 32769, 0) == 0 and f(6, 64, 4) == 0 and f(6, 64, -1) == 0
-    for rows in (0, 1, 16, 17, 1003, 8192, 65536, 10 ** 7):
-        for cols in (1, 64, 7168, 32768):
-            for gate in (0, 1, rows):
-                n = f(rows, cols, gate)
-                assert n > 0 and n % 256 == 0 and n >= 16 * rows + 4 * cols * gate * (rows > 0)
-                assert gate or n <= 16 * rows + 4 * 4 * (2100 * max(cols, 512) + 512)   # a bound on the runs that the rows do not move
+    assert f(3, 6, 64, 0) == 0 and f(0, -1, 64, 0) == 0 and f(0, 6, 0, 0) == 0 and f(0, 6, 32769, 0) == 0 and f(0, 6, 64, 4) == 0 and f(0, 6, 64, -1) == 0
+    for dtype in (0, 1, 2):
+        for cols in (1, 63, 64, 2048, 7168, 8192, 8193, 32768):
+            for rows in (0, 1, 16, 17, 1003, 8192, 65536, 10 ** 7):
+                n = f(dtype, rows, cols, 0)
+                wide = 16 * rows if cols < 8 or cols > 8192 else 0
+                assert n > 0 and n % 256 == 0 and n <= wide + 4 * 4 * (2100 * max(cols, 512) + 512)   # a bound that the rows do not move, but for their means
+                # a gate of few rows has partial sums of its own, one of many is written as it is
+                assert f(dtype, rows, cols, 1) >= n and f(dtype, rows, cols, rows) <= n + 4 * 4 * 2100 * max(cols, 512)
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not real")

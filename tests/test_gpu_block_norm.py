@@ -195,7 +195,7 @@ def run(c):
     return f
 
 
-SIZES = [(1, 1), (1, 7168), (2, 8), (3, 33), (5, 128), (7, 129), (16, 512), (17, 513), (63, 1000), (33, 2048), (9, 2049), (20, 4095), (12, 5001), (6, 8192), (11, 8200), (5, 12289), (4, 16384),
+SIZES = [(1, 1), (1, 7168), (2, 8), (3, 33), (5, 128), (7, 129), (70, 600), (9, 1024), (40, 400), (16, 512), (17, 513), (63, 1000), (33, 2048), (9, 2049), (20, 4095), (12, 5001), (6, 8192), (11, 8200), (5, 12289), (4, 16384),
          (3, 20000), (2, 32768), (1500, 96), (4100, 200)]
 
 

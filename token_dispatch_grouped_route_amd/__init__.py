@@ -108,7 +108,7 @@ def lib():
         L.moe_linear_forward.argtypes = [i32] * 7 + [P, i64, P, i64, i32, P, P, i64, P, i64, P, i64, P, size, P]
         L.moe_linear_backward.argtypes = [i32] * 7 + [P, i64, P, i64, P, i64, i32, P, i64, P, i64, P, i64, P, P, size, P]
         L.moe_block_norm_forward.argtypes = [i32] * 5 + [i64, i32, P, i64, P, i64, f32, f32, P, P, P, i64, P, P, f32, P, i64, P, i64, P, P, P, P, P]
-        L.moe_block_norm_workspace_bytes.argtypes = [i64, i32, i64]
+        L.moe_block_norm_workspace_bytes.argtypes = [i32, i64, i32, i64]
         L.moe_block_norm_backward.argtypes = ([i32] * 5 + [i64, i32] + [P, i64] * 4 + [f32, f32, P, P, P, i64] + [P] * 5 + [P, i64] * 2 + [P] * 6 + [size, P])
         L.moe_few_workspace_bytes.argtypes = [S]
         L.moe_forward_few.argtypes = [S] + [P] * 6 + [size, P, P]
@@ -998,7 +998,7 @@ def block_norm_backward(dr, dn, r, b, stats, kind="rms", post=None, gate=None, p
         grads = tuple(made[name] for name in _BLOCK_NORM_GRADS)
         if all(g is None for g in grads):
             return grads
-        nbytes = int(lib().moe_block_norm_workspace_bytes(rows, cols, gate_rows))
+        nbytes = int(lib().moe_block_norm_workspace_bytes(_code(_DTYPE, b.dtype, "b.dtype"), rows, cols, gate_rows))
         ws = torch.empty(nbytes, dtype=torch.uint8, device=b.device)
         dx, db = grads[:2]
         _check(lib().moe_block_norm_backward(_code(_KIND, kind, "kind"), bool(post) + 2 * bool(pre), _code(_DTYPE, b.dtype, "b.dtype"), _code(_DTYPE, r.dtype, "r.dtype"),

@@ -835,9 +835,9 @@ int32_t moe_block_norm_forward(int32_t kind, int32_t parts, int32_t dtype, int32
     return launched(launch_block_norm_fwd(a, dtype, sdtype, wdtype, static_cast<hipStream_t>(stream)));
 }
 
-size_t moe_block_norm_workspace_bytes(int64_t rows, int32_t cols, int64_t gate_rows) {
-    if (check_norm(MOE_LAYER_NORM, MOE_FP32, MOE_FP32, rows, cols) != MOE_OK || gate_rows < 0 || (gate_rows > 0 && rows % gate_rows != 0)) return 0;
-    return block_norm_bwd_bytes(rows, cols, gate_rows);
+size_t moe_block_norm_workspace_bytes(int32_t dtype, int64_t rows, int32_t cols, int64_t gate_rows) {
+    if (check_norm(MOE_LAYER_NORM, dtype, dtype, rows, cols) != MOE_OK || gate_rows < 0 || (gate_rows > 0 && rows % gate_rows != 0)) return 0;
+    return block_norm_bwd_bytes(rows, cols, gate_rows, elem_bytes(dtype));
 }
 
 int32_t moe_block_norm_backward(int32_t kind, int32_t parts, int32_t dtype, int32_t sdtype, int32_t wdtype, int64_t rows, int32_t cols,
@@ -872,7 +872,7 @@ int32_t moe_block_norm_backward(int32_t kind, int32_t parts, int32_t dtype, int3
         !aligned_to(dpre_bias, wdtype) || !aligned4(post_mean) || !aligned4(post_rstd) || !aligned4(pre_mean) || !aligned4(pre_rstd) ||
         (reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) != 0)
         return MOE_ERR_ALIGN;
-    if (ws_bytes < moe_block_norm_workspace_bytes(rows, cols, gate_rows)) return MOE_ERR_WORKSPACE;
+    if (ws_bytes < moe_block_norm_workspace_bytes(dtype, rows, cols, gate_rows)) return MOE_ERR_WORKSPACE;
     if (!is_gfx950()) return MOE_ERR_DEVICE;
     if (rows == 0) a.gate_share = gate_rows;
     a.dr = dr, a.lddr = lddr, a.dn = dn, a.lddn = lddn, a.r = const_cast<void*>(dn ? r : nullptr), a.ldr = ldr, a.b = needs_b ? b : nullptr;

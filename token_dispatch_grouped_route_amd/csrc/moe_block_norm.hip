@@ -7,36 +7,37 @@
 namespace moe {
 namespace {
 
-// N elements of type X (N that of a 16-byte chunk of another type) in 16-byte pieces.
-template <typename X, int N> struct Pieces {
-    static constexpr int P = N / Chunk<X>::N;
-    u32x4_t raw[P];
-    __device__ __forceinline__ void load(const X* p, int valid) {
-#pragma unroll
-        for (int h = 0; h < P; ++h) raw[h] = load_chunk<X>(p + h * Chunk<X>::N, valid - h * Chunk<X>::N);
+// A vector of a team's columns: held in registers, or, where a thread has many chunks, read from the caches row by row.
+template <typename WT, int N, int NV, int TPR, bool HELD> struct FwdVector {
+    NormWeights<WT, N, HELD ? NV : 1, TPR> v;
+    const WT* p;
+    float none;
+    __device__ __forceinline__ void load(const void* w, int tid, int cols, float fill) {
+        p = static_cast<const WT*>(w);
+        none = fill;
+        if constexpr (HELD) v.load(w, tid, cols, fill);
     }
-    __device__ __forceinline__ void get(float (&f)[N]) const {
+    __device__ __forceinline__ void get(int j, int c, int cols, float (&f)[N]) {
+        if constexpr (HELD) {
 #pragma unroll
-        for (int h = 0; h < P; ++h) {
-            float part[Chunk<X>::N];
-            unpack_chunk<X>(raw[h], part);
+            for (int h = 0; h < NormWeights<WT, N, 1, TPR>::P; ++h) renew(v.raw[j][h]);
+            v.get(j, f);
+        } else if (p) {
+            Pieces<WT, N> q;
+            q.load(p + c, cols - c);
+            q.get(f);
+        } else {
 #pragma unroll
-            for (int i = 0; i < Chunk<X>::N; ++i) f[h * Chunk<X>::N + i] = part[i];
-        }
-    }
-    static __device__ __forceinline__ void put(X* p, const float (&f)[N], int valid) {
-#pragma unroll
-        for (int h = 0; h < P; ++h) {
-            float part[Chunk<X>::N];
-#pragma unroll
-            for (int i = 0; i < Chunk<X>::N; ++i) part[i] = f[h * Chunk<X>::N + i];
-            store_chunk<X>(p + h * Chunk<X>::N, pack_chunk<X>(part), valid - h * Chunk<X>::N);
+            for (int i = 0; i < N; ++i) f[i] = none;
         }
     }
 };
+// Waves a SIMD that the registers are cut down to: four where a thread has two chunks and everything is 16-bit, which leaves
+// two workgroups of 512 a CU instead of one (with a stream in fp32 that spills: 8192 x 7168 140 to 155 us).
+template <typename D, typename R, typename WT, int TPR, int NV> constexpr int fwd_waves() { return TPR == 1024 || (NV <= 2 && sizeof(WT) == sizeof(D) && sizeof(R) == sizeof(D)) ? 4 : 2; }
 
 template <typename D, typename R, typename WT, int TPR, int NV>
-__global__ __launch_bounds__(norm_block(TPR)) void block_norm_fwd_kernel(BlockNorm a) {
+__global__ __launch_bounds__(norm_block(TPR), (fwd_waves<D, R, WT, TPR, NV>())) void block_norm_fwd_kernel(BlockNorm a) {
     constexpr int N = Chunk<D>::N, BLOCK = norm_block(TPR), W = norm_waves(TPR);
     static_assert(sizeof(R) >= sizeof(D), "a stream at least as wide as the block's output");
     __shared__ float lds[8 * W];   // four sums per row, each in two buffers
@@ -58,7 +59,7 @@ __global__ __launch_bounds__(norm_block(TPR)) void block_norm_fwd_kernel(BlockNo
         }
     };
     fetch(row);
-    NormWeights<WT, N, NV, TPR> w1, c1, w2, c2, gate;
+    FwdVector<WT, N, NV, TPR, (NV <= 2)> w1, c1, w2, c2, gate;
     w1.load(a.post_weight, tid, cols, 1.0f);
     c1.load(a.post_bias, tid, cols, 0.0f);
     w2.load(a.pre_weight, tid, cols, 1.0f);
@@ -95,11 +96,12 @@ __global__ __launch_bounds__(norm_block(TPR)) void block_norm_fwd_kernel(BlockNo
         rstd = q[0] < __builtin_inff() ? 1.0f / sqrtf(q[0] / static_cast<float>(cols) + a.eps) : __builtin_nanf("");   // as the row norm
     };
     for (int64_t base = row0; base < a.rows; base += step, row += step) {
-        float v[NV][N], fx[NV][N], mean, rstd;
+        float v[NV][N], mean, rstd;
+        Pieces<R, N> x_now[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             unpack_chunk<D>(nb[j], v[j]);
-            nx[j].get(fx[j]);
+            x_now[j] = nx[j];
         }
         if (base + step < a.rows) fetch(row + step);
         if (gates && in(row) / a.gate_share != held) {
@@ -115,8 +117,8 @@ __global__ __launch_bounds__(norm_block(TPR)) void block_norm_fwd_kernel(BlockNo
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 float w[N], c[N];
-                w1.get(j, w);
-                c1.get(j, c);
+                w1.get(j, (j * TPR + tid) * N, cols, w);
+                c1.get(j, (j * TPR + tid) * N, cols, c);
 #pragma unroll
                 for (int i = 0; i < N; ++i) v[j][i] = v[j][i] * rstd * w[i] + c[i];
             }
@@ -125,12 +127,16 @@ __global__ __launch_bounds__(norm_block(TPR)) void block_norm_fwd_kernel(BlockNo
         for (int j = 0; j < NV; ++j) {
             if (gates) {
                 float g[N];
-                gate.get(j, g);
+                gate.get(j, (j * TPR + tid) * N, cols, g);
 #pragma unroll
                 for (int i = 0; i < N; ++i) v[j][i] *= g[i];
             }
+            float fx[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[j][i] = a.x_scale * fx[j][i] + a.scale * v[j][i];
+            for (int h = 0; h < Pieces<R, N>::P; ++h) renew(x_now[j].raw[h]);
+            x_now[j].get(fx);
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[j][i] = a.x_scale * fx[i] + a.scale * v[j][i];
             const int c = (j * TPR + tid) * N;
             if (row < a.rows) Pieces<R, N>::put(static_cast<R*>(a.r) + row * a.ldr + c, v[j], cols - c);
         }
@@ -152,8 +158,8 @@ __global__ __launch_bounds__(norm_block(TPR)) void block_norm_fwd_kernel(BlockNo
                 for (int j = 0; j < NV; ++j) {
                     const int at = (j * TPR + tid) * N;
                     float w[N], c[N], o[N];
-                    w2.get(j, w);
-                    c2.get(j, c);
+                    w2.get(j, at, cols, w);
+                    c2.get(j, at, cols, c);
 #pragma unroll
                     for (int i = 0; i < N; ++i) o[i] = v[j][i] * rstd * w[i] + c[i];
                     store_chunk<D>(static_cast<D*>(a.n) + row * a.ldn + at, pack_chunk<D>(o), cols - at);
@@ -165,14 +171,16 @@ __global__ __launch_bounds__(norm_block(TPR)) void block_norm_fwd_kernel(BlockNo
 }
 
 // Calls f with a team for rows of `chunks` 16-byte chunks of b; false if they are too long for any.
-template <typename F> bool with_team(int64_t chunks, F&& f) {
+template <typename D, typename F> bool with_team(int64_t chunks, F&& f) {
     if (chunks <= 16) f(Geo<16, 1>{});
     else if (chunks <= 64) f(Geo<64, 1>{});
+    else if (chunks <= 128) f(Geo<128, 1>{});
     else if (chunks <= 256) f(Geo<256, 1>{});
     else if (chunks <= 512) f(Geo<256, 2>{});
     else if (chunks <= 1024) f(Geo<512, 2>{});
-    else if (chunks <= 2048) f(Geo<1024, 2>{});
-    else if (chunks <= 4096) f(Geo<1024, 4>{});
+    else if (sizeof(D) == 4 && chunks <= 2048) f(Geo<1024, 2>{});
+    else if (chunks <= 2048) f(Geo<512, 4>{});
+    else if (chunks <= 4096) f(Geo<512, 8>{});
     else if (chunks <= 8192) f(Geo<1024, 8>{});
     else return false;
     return true;
@@ -188,9 +196,9 @@ hipError_t launch_block_norm_fwd(const BlockNorm& a, int dtype, int sdtype, int 
         using WT = decltype(wt);
         auto go = [&](auto stream) {
             using R = decltype(stream);
-            done = with_team(norm_chunks(a.cols, sizeof(D)), [&](auto geo) {
+            done = with_team<D>(norm_chunks(a.cols, sizeof(D)), [&](auto geo) {
                 using G = decltype(geo);
-                if constexpr (sizeof(D) == 4 || G::nv < 8) {   // 16-bit rows end at 4096 chunks
+                if constexpr (sizeof(D) == 4 ? G::nv != 4 : G::tpr < 1024) {   // the teams of this type
                     constexpr int block = norm_block(G::tpr), teams = block / G::tpr;
                     const int64_t want = (a.rows + teams - 1) / teams, cap = static_cast<int64_t>(device_cu_count()) * (2048 / block);
                     block_norm_fwd_kernel<D, R, WT, G::tpr, G::nv><<<static_cast<int>(want < cap ? want : cap), block, 0, s>>>(a);

@@ -1,4 +1,5 @@
-// Block norm, backward: moe_block_norm.h has the formulas.  Two launches over the rows:
+// Block norm, backward: moe_block_norm.h has the formulas.  Rows of 8 to 8192 elements are held in registers, in one
+// launch (moe_block_norm_row.h); others in two launches over the rows:
 //
 //   rows      the four means that N' takes for the two norms, from one pass over each row.  The post norm's follow from sums
 //             that do not wait for the pre norm's: with g = dn w2, q = gate w1, t = dr + rstd2 (g - m0 - N(r) m1),
@@ -101,41 +102,6 @@ template <typename T> __global__ __launch_bounds__(256) void block_norm_rows_ker
     }
 }
 
-// How the rows are cut into runs of a workgroup.  Runs stay inside one row of the gate, or hold whole ones, so that
-// the gate's sums are over rows of one run (per_gate = 1: complete), or over per_gate runs.
-struct Runs {
-    int64_t runs, length, per_gate;   // length: rows of a run, the last of a gate's may be shorter
-    int64_t share;                    // rows per row of the gate
-    __host__ __device__ void range(int64_t run, int64_t rows, int64_t& r0, int64_t& r1) const {
-        const int64_t first = run / per_gate * (per_gate > 1 ? share : length), end = per_gate > 1 ? first + share : rows;
-        r0 = first + run % per_gate * length;
-        r1 = r0 + length < end ? r0 + length : end;
-    }
-};
-Runs runs_of(int64_t rows, int cols, int64_t gate_rows) {
-    const int64_t strips = (cols + 511) / 512, target = strips > 1024 ? 1 : 1024 / strips;   // runs wanted
-    const int64_t even = (rows + target - 1) / target, length = even < 16 ? 16 : even, share = gate_rows > 0 ? rows / gate_rows : rows;
-    Runs r;
-    r.share = share;
-    if (share >= length) {   // a gate row's rows in per_gate runs
-        r.per_gate = (share + length - 1) / length;
-        r.length = (share + r.per_gate - 1) / r.per_gate;
-        r.per_gate = (share + r.length - 1) / r.length;
-        if (r.per_gate == 1) r.runs = (rows + r.length - 1) / r.length;
-        else r.runs = rows / share * r.per_gate;
-    } else {   // whole gate rows
-        r.per_gate = 1;
-        r.length = length / share * share;
-        r.runs = (rows + r.length - 1) / r.length;
-    }
-    return r;
-}
-
-// Partial sums of a strip of columns: [runs, cols] each, the gate's [gate rows, per_gate, cols].
-struct Partials {
-    float *gate, *post_weight, *post_bias, *pre_weight, *pre_bias;
-};
-
 template <typename T> __global__ __launch_bounds__(256) void block_norm_columns_kernel(BlockNorm a, const float4* means, Runs runs, Partials part) {
     __shared__ __align__(16) float join[4][512];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 512 + 8 * lane, valid = a.cols - c;
@@ -146,15 +112,20 @@ template <typename T> __global__ __launch_bounds__(256) void block_norm_columns_
     read_vector<T>(a.post_weight, c, a.w_f32, valid, 1.0f, w1);
     read_vector<T>(a.post_bias, c, a.w_f32, valid, 0.0f, c1);
     float s_w2[8] = {}, s_c2[8] = {}, s_w1[8] = {}, s_c1[8] = {}, s_g[8] = {};
-    // adds the waves' sums of these columns and writes them to a row of `to`
-    auto leave = [&](float* to, const float (&sum)[8]) {
-        if (!to) return;   // the same for the whole launch
+    // adds the waves' sums of these columns and writes them to a row of `to`, or in the vectors' type to row `row` of the gate's gradient
+    auto leave = [&](float* to, const float (&sum)[8], int64_t row = -1) {
+        if (!to && row < 0) return;   // the same for the whole launch
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 8; ++i) join[wave][8 * lane + i] = sum[i];
         __syncthreads();
         for (int i = threadIdx.x; i < 512; i += 256)
-            if (static_cast<int>(blockIdx.x) * 512 + i < a.cols) to[blockIdx.x * 512 + i] = join[0][i] + join[1][i] + join[2][i] + join[3][i];
+            if (const int at = static_cast<int>(blockIdx.x) * 512 + i; at < a.cols) {
+                const float v = join[0][i] + join[1][i] + join[2][i] + join[3][i];
+                if (to) to[at] = v;
+                else if (a.w_f32) static_cast<float*>(a.dgate)[row * a.cols + at] = v;
+                else static_cast<T*>(a.dgate)[row * a.cols + at] = from_f32<T>(v);
+            }
     };
     for (int64_t g0 = r0; g0 < r1;) {   // the rows of one row of the gate
         const int64_t gate = g0 / runs.share, g1 = min(r1, (gate + 1) * runs.share);
@@ -189,7 +160,7 @@ template <typename T> __global__ __launch_bounds__(256) void block_norm_columns_
                 if (a.db) store8<T>(a.db, row * a.lddb + c, a.b_f32, valid, o);
             }
         }
-        leave(part.gate ? part.gate + (gate * runs.per_gate + (runs.per_gate > 1 ? blockIdx.y % runs.per_gate : 0)) * a.cols : nullptr, s_g);
+        leave(part.gate ? part.gate + (gate * runs.per_gate + blockIdx.y % runs.per_gate) * a.cols : nullptr, s_g, a.dgate && !part.gate ? gate : -1);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s_g[i] = 0.0f;
         g0 = g1;
@@ -202,14 +173,44 @@ template <typename T> __global__ __launch_bounds__(256) void block_norm_columns_
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+Runs columns_runs(int64_t rows, int cols, int64_t gate_rows) { return runs_of(rows, gate_rows, 1024 / ((cols + 511) / 512), 16); }   // four workgroups a CU
 
 }  // namespace
 
-// The rows' means, then five sets of partial sums.
-size_t block_norm_bwd_bytes(int64_t rows, int cols, int64_t gate_rows) {
+Runs runs_of(int64_t rows, int64_t gate_rows, int64_t target, int64_t least) {
+    const int64_t even = (rows + target - 1) / target, length = even < least ? least : even, share = gate_rows > 0 ? rows / gate_rows : rows;
+    Runs r;
+    r.share = share;
+    if (share >= length) {   // a gate row's rows in per_gate runs
+        r.per_gate = (share + length - 1) / length;
+        r.length = (share + r.per_gate - 1) / r.per_gate;
+        r.per_gate = (share + r.length - 1) / r.length;
+        if (r.per_gate == 1) r.runs = (rows + r.length - 1) / r.length;
+        else r.runs = rows / share * r.per_gate;
+    } else {   // whole gate rows
+        r.per_gate = 1;
+        r.length = length / share * share;
+        r.runs = (rows + r.length - 1) / r.length;
+    }
+    return r;
+}
+
+
+// Rows that a team holds in registers, 8 to 8192 elements: two workgroups of 256 threads a CU or one of 512, at least four
+// rows each.
+Runs block_norm_row_runs(int64_t rows, int cols, int64_t gate_rows, int elem_bytes) {
+    if (cols < 8 || cols > 8192 || rows == 0) return Runs{};
+    return runs_of(rows, gate_rows, norm_chunks(cols, elem_bytes) > 256 ? 256 : 512, norm_chunks(cols, elem_bytes) > 64 ? 4 : 16);
+}
+
+// The rows' means where two launches share the work, then five sets of partial sums.
+static size_t bytes_of(const Runs& r, bool means, int64_t rows, int cols, int64_t gate_rows) {
+    return (means ? align256(rows * 16) : 0) + 4 * align256(r.runs * cols * 4) + align256((gate_rows > 0 && r.per_gate > 1 ? gate_rows * r.per_gate : 0) * cols * 4);
+}
+size_t block_norm_bwd_bytes(int64_t rows, int cols, int64_t gate_rows, int elem_bytes) {
     if (rows == 0) return 256;
-    const Runs r = runs_of(rows, cols, gate_rows);
-    return align256(rows * 16) + 4 * align256(r.runs * cols * 4) + align256((gate_rows > 0 ? gate_rows * r.per_gate : 0) * cols * 4);
+    const Runs row = block_norm_row_runs(rows, cols, gate_rows, elem_bytes);
+    return row.runs ? bytes_of(row, false, rows, cols, gate_rows) : bytes_of(columns_runs(rows, cols, gate_rows), true, rows, cols, gate_rows);
 }
 
 hipError_t launch_block_norm_bwd(const BlockNorm& a, int dtype, int wdtype, hipStream_t s) {
@@ -225,22 +226,29 @@ hipError_t launch_block_norm_bwd(const BlockNorm& a, int dtype, int wdtype, hipS
     Partials part = {};
     auto job = [&](int i, float* p, void* out, int64_t groups, int64_t slots) { sums.sum[i] = {p, out}, sums.groups[i] = groups, sums.slots[i] = slots; };
     if (a.rows > 0) {
-        const Runs runs = runs_of(a.rows, a.cols, gate_rows);
-        float4* means = reinterpret_cast<float4*>(take(true, a.rows * 16));
+        Runs runs = block_norm_row_runs(a.rows, a.cols, gate_rows, dtype == MOE_FP32 ? 4 : 2);
+        const bool row = runs.runs > 0;
+        if (!row) runs = columns_runs(a.rows, a.cols, gate_rows);
+        float4* means = reinterpret_cast<float4*>(take(!row, a.rows * 16));
         const size_t bytes = static_cast<size_t>(runs.runs) * a.cols * 4;
         part.pre_weight = take(a.dpre_weight, bytes);
         part.pre_bias = take(a.dpre_bias, bytes);
         part.post_weight = take(a.dpost_weight, bytes);
         part.post_bias = take(a.dpost_bias, bytes);
-        part.gate = take(a.dgate, static_cast<size_t>(gate_rows) * runs.per_gate * a.cols * 4);
-        auto go = [&](auto t) {
-            using T = decltype(t);
-            block_norm_rows_kernel<T><<<static_cast<unsigned>(a.rows < 4096 ? a.rows : 4096), 256, 0, s>>>(a, means);
-            block_norm_columns_kernel<T><<<dim3((a.cols + 511) / 512, static_cast<unsigned>(runs.runs)), 256, 0, s>>>(a, means, runs, part);
-        };
-        if (dtype == MOE_FP16) go(fp16_t{});
-        else go(bf16_t{});
-        const hipError_t e = hipGetLastError();
+        part.gate = take(a.dgate && runs.per_gate > 1, static_cast<size_t>(gate_rows) * runs.per_gate * a.cols * 4);
+        hipError_t e;
+        if (row) {
+            e = dtype == MOE_BF16 ? launch_block_norm_row_bf16(a, runs, part, s) : dtype == MOE_FP16 ? launch_block_norm_row_fp16(a, runs, part, s) : launch_block_norm_row_fp32(a, runs, part, s);
+        } else {
+            auto go = [&](auto t) {
+                using T = decltype(t);
+                block_norm_rows_kernel<T><<<static_cast<unsigned>(a.rows < 4096 ? a.rows : 4096), 256, 0, s>>>(a, means);
+                block_norm_columns_kernel<T><<<dim3((a.cols + 511) / 512, static_cast<unsigned>(runs.runs)), 256, 0, s>>>(a, means, runs, part);
+            };
+            if (dtype == MOE_FP16 || (dtype == MOE_FP32 && wdtype == MOE_FP16)) go(fp16_t{});
+            else go(bf16_t{});
+            e = hipGetLastError();
+        }
         if (e != hipSuccess) return e;
         job(0, part.pre_weight, a.dpre_weight, 1, runs.runs);
         job(1, part.pre_bias, a.dpre_bias, 1, runs.runs);
@@ -255,7 +263,9 @@ hipError_t launch_block_norm_bwd(const BlockNorm& a, int dtype, int wdtype, hipS
         job(3, a.dpost_bias ? any : nullptr, a.dpost_bias, 1, 0);
         job(4, a.dgate ? any : nullptr, a.dgate, a.gate_share, 0);   // gate_share holds the gate's rows here
     }
-    if (a.dpre_weight || a.dpre_bias || a.dpost_weight || a.dpost_bias || a.dgate) {
+    bool any = false;
+    for (const ColumnSum& c : sums.sum) any = any || c.part;
+    if (any) {
         if (wdtype == MOE_FP32) launch_column_sums<float>(sums, s);
         else if (wdtype == MOE_BF16) launch_column_sums<bf16_t>(sums, s);
         else launch_column_sums<fp16_t>(sums, s);
