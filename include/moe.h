@@ -486,7 +486,7 @@ int32_t moe_forward_w4(const moe_shape* shape, int32_t dtype, int32_t group, con
 typedef enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_SILU = 3, MOE_ACT_SWIGLU = 4 } moe_act;
 
 /* Bytes of ws for moe_linear_forward (backward = 0) or moe_linear_backward (1); a pure function, 0 for invalid
- * sizes. */
+ * sizes.  256 for a forward that needs none (ws may then be NULL). */
 size_t moe_linear_workspace_bytes(int32_t act, int32_t M, int32_t N, int32_t K, int32_t backward);
 
 /*

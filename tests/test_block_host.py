@@ -25,8 +25,8 @@ def linear_bwd(dtype=0, bdtype=0, odtype=0, act=3, M=4, N=32, K=64, dy=A, lddy=3
     (dict(M=(1 << 24) + 1), SHAPE), (dict(N=0), SHAPE), (dict(N=(1 << 20) + 1, ldw=1 << 21, ldy=1 << 21, ldr=1 << 21, ldz=1 << 21), SHAPE), (dict(K=0), SHAPE),
     (dict(M=1 << 24, N=1 << 20, ldw=1 << 20, ldy=1 << 20, ldr=1 << 20, ldz=1 << 20), SHAPE), (dict(ldx=63), SHAPE), (dict(ldw=31), SHAPE), (dict(by_column=1), SHAPE),
     (dict(ldy=31), SHAPE), (dict(ldr=31), SHAPE), (dict(ldz=31), SHAPE), (dict(act=4, ldw=64), SHAPE), (dict(x=None), NULL), (dict(w=None), NULL), (dict(y=None), NULL),
-    (dict(ws=None), NULL), (dict(y=A), SHAPE), (dict(y=B), SHAPE), (dict(z=A), SHAPE), (dict(z=D), SHAPE), (dict(z=C), SHAPE), (dict(res=D, ldr=40), SHAPE), (dict(x=A + 1), ALIGN),
-    (dict(w=B + 1), ALIGN), (dict(bias=C + 1), ALIGN), (dict(bdtype=2, bias=C + 2), ALIGN), (dict(odtype=2, y=D + 2), ALIGN), (dict(odtype=2, res=C + 2), ALIGN), (dict(ws=A + 64), ALIGN), (dict(n=8), WORKSPACE),
+    (dict(ws=None, K=8192, ldx=8192), NULL), (dict(y=A), SHAPE), (dict(y=B), SHAPE), (dict(z=A), SHAPE), (dict(z=D), SHAPE), (dict(z=C), SHAPE), (dict(res=D, ldr=40), SHAPE), (dict(x=A + 1), ALIGN),
+    (dict(w=B + 1), ALIGN), (dict(bias=C + 1), ALIGN), (dict(bdtype=2, bias=C + 2), ALIGN), (dict(odtype=2, y=D + 2), ALIGN), (dict(odtype=2, res=C + 2), ALIGN), (dict(ws=A + 64), ALIGN), (dict(n=8, K=8192, ldx=8192), WORKSPACE),
 ])
 def test_linear_refusals(bad, status):
     assert linear(**bad) == status

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch  # loads the HIP runtime that the library then shares (same soname)
@@ -798,15 +799,17 @@ def _address(t):
 
 
 def _scratch(nbytes, like, ws=None):
-    """A workspace of nbytes on like's GPU, or the caller's, checked."""
+    """A workspace of nbytes on like's GPU (None for 256, which stand for none), or the caller's, checked."""
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes > 256 else None
     if not isinstance(ws, torch.Tensor) or ws.device != like.device or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
         raise MoeError("ws must be a contiguous tensor of at least %d bytes on %s" % (nbytes, like.device))
     return ws
 
 
+@functools.lru_cache(maxsize=4096)
 def linear_workspace_bytes(M, N, K, act=None, backward=False) -> int:
+    """Bytes of ws for linear_forward or linear_backward of these sizes; at most 256 stand for none."""
     n = int(lib().moe_linear_workspace_bytes(_code(_ACT, act, "act"), M, N, K, bool(backward)))
     if n == 0:
         raise MoeError("invalid sizes M = %d, N = %d, K = %d for the linear map" % (M, N, K))
@@ -833,18 +836,20 @@ def linear_forward(x, w, bias=None, act=None, residual=None, out_dtype=None, y=N
         shape = x.shape[:-1] + (N,)
         if y is None:
             y = torch.empty(shape, dtype=out, device=x.device)
-        elif y.dtype != out:
-            raise MoeError("y is %s, out_dtype %s" % (y.dtype, out))
-        py, ldy = _rows(y, "y", y, shape)[:2]
-        if y.device != x.device:
-            raise MoeError("y is on %s, x on %s" % (y.device, x.device))
+            py, ldy = y.data_ptr(), N
+        else:
+            if y.dtype != out:
+                raise MoeError("y is %s, out_dtype %s" % (y.dtype, out))
+            py, ldy = _rows(y, "y", y, shape)[:2]
+            if y.device != x.device:
+                raise MoeError("y is on %s, x on %s" % (y.device, x.device))
         pr, ldr = _rows(residual, "residual", y, shape)[:2] if residual is not None else (None, N)
         z = torch.empty(x.shape[:-1] + (C,), dtype=x.dtype, device=x.device) if keep and act is not None else None
         nbytes = linear_workspace_bytes(M, N, K, act)
         ws = _scratch(nbytes, x, ws)
         _check(lib().moe_linear_forward(_code(_DTYPE, x.dtype, "x.dtype"), _code(_DTYPE, bd, "bias.dtype"), _code(_DTYPE, out, "out_dtype"), code, M, N, K,
                                         px, ldx, pw, ldw, by_column, _like(bias, bd, "bias", (C,), dev), pr, ldr, py, ldy, _address(z), C,
-                                        ws.data_ptr(), nbytes, _handle(dev)), "moe_linear_forward")
+                                        _address(ws), nbytes, _handle(dev)), "moe_linear_forward")
     return y, z
 
 
@@ -877,7 +882,7 @@ def linear_backward(dy, x, w, z=None, act=None, bias=False, dx=True, dw=True, ws
         ws = _scratch(nbytes, x, ws)
         _check(lib().moe_linear_backward(_code(_DTYPE, x.dtype, "x.dtype"), _code(_DTYPE, bd, "bias"), _code(_DTYPE, dy.dtype, "dy.dtype"), code, M, N, K,
                                          pdy, lddy, px, ldx, pw, ldw, by_column, pz, ldz, _address(gx), K, _address(gw), K if by_column else C,
-                                         _address(gb), ws.data_ptr(), nbytes, _handle(dev)), "moe_linear_backward")
+                                         _address(gb), _address(ws), nbytes, _handle(dev)), "moe_linear_backward")
     return gx, gw, gb
 
 
@@ -913,17 +918,17 @@ def linear(x, w, bias=None, act=None, residual=None, out_dtype=None):
 def _vectors(x, post, gate, pre):
     """(dtype, gate rows, addresses of post's weight and bias, the gate, pre's weight and bias) of a block norm's
     vectors on x's GPU, all of one dtype."""
-    dev, cols = x.get_device(), x.shape[-1]
-    five = (post or (None, None)) + ((gate,) if gate is not None else (None,)) + (pre or (None, None))
-    wd = next((t.dtype for t in five if isinstance(t, torch.Tensor)), x.dtype)
-    gate_rows, shape = 0, None
+    dev, cols = x.get_device(), (x.shape[-1],)
+    (w1, c1), (w2, c2) = post or (None, None), pre or (None, None)
+    wd = next((t.dtype for t in (w1, gate, w2, c1, c2) if isinstance(t, torch.Tensor)), x.dtype)
+    gate_rows = 0
     if gate is not None:
         if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2):
             raise MoeError("gate must be [C] or [G, C]")
         gate_rows = gate.shape[0] if gate.dim() == 2 else 1
-        shape = gate.shape[:-1] + (cols,)
-    names = ("post weight", "post bias", "gate", "pre weight", "pre bias")
-    return wd, gate_rows, [_like(t, wd, n, shape if n == "gate" else (cols,), dev) for n, t in zip(names, five)]
+        gate = _like(gate, wd, "gate", gate.shape[:-1] + cols, dev)
+    return wd, gate_rows, (_like(w1, wd, "post weight", cols, dev), _like(c1, wd, "post bias", cols, dev), gate, _like(w2, wd, "pre weight", cols, dev),
+                           _like(c2, wd, "pre bias", cols, dev))
 
 
 def _pair(norm, name):
@@ -952,15 +957,18 @@ def block_norm_forward(x, b, kind="rms", post=None, gate=None, pre=None, eps=1e-
         wd, gate_rows, vec = _vectors(b, post, gate, pre)
         if r is None:
             r = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        pr, ldr = _rows(r, "r", x, x.shape)[:2]
-        if pre is None:
-            if n is not None:
-                raise MoeError("n is written with a norm of r only")
-            pn, ldn = None, cols
+            pr, ldr = r.data_ptr(), cols
         else:
-            if n is None:
-                n = torch.empty(b.shape, dtype=b.dtype, device=x.device)
+            pr, ldr = _rows(r, "r", x, x.shape)[:2]
+        if n is not None:
+            if pre is None:
+                raise MoeError("n is written with a norm of r only")
             pn, ldn = _rows(n, "n", b, b.shape)[:2]
+        elif pre is not None:
+            n = torch.empty(b.shape, dtype=b.dtype, device=x.device)
+            pn, ldn = n.data_ptr(), cols
+        else:
+            pn, ldn = None, cols
         stat = lambda wanted: torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if wanted else None
         layer = kind == "layer"
         stats = (stat(post and layer), stat(post), stat(pre and layer), stat(pre))

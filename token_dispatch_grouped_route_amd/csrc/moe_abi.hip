@@ -716,12 +716,13 @@ int32_t moe_linear_forward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_
         (z && bad_ld(ldz, M, s.C)))
         return MOE_ERR_SHAPE;
     if (M == 0) return MOE_OK;
-    if (!x || !w || !y || !ws) return MOE_ERR_NULL;
+    const size_t need = moe_linear_workspace_bytes(act, M, N, K, 0);
+    if (!x || !w || !y || (!ws && need > kWsAlign)) return MOE_ERR_NULL;
     if (y == x || y == w || z == x || z == w || z == y || (residual == y && ldr != ldy) || (residual && residual == z)) return MOE_ERR_SHAPE;
     if (!aligned_to(x, dtype) || !aligned_to(w, dtype) || !aligned_to(bias, bdtype) || !aligned_to(residual, odtype) || !aligned_to(y, odtype) ||
         !aligned_to(z, dtype) || (reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) != 0)
         return MOE_ERR_ALIGN;
-    if (ws_bytes < moe_linear_workspace_bytes(act, M, N, K, 0)) return MOE_ERR_WORKSPACE;
+    if (need > kWsAlign && ws_bytes < need) return MOE_ERR_WORKSPACE;
     if (!is_gfx950()) return MOE_ERR_DEVICE;
     Product g = {};
     g.M = M, g.N = static_cast<int32_t>(s.C), g.K = K, g.b_strided = !w_by_column;

@@ -43,6 +43,16 @@ hipError_t launch_linear_slope(const LinearSlope& a, int dtype, int bdtype, void
 // Bytes that launch_product may write at `part` for a product of these sizes.
 size_t product_part_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_product(Product g, int dtype, void* part, hipStream_t s);
+// The products of 1 to kLinearRows rows whose A has the reduction contiguous (moe_linear_rows.hip), without workspace.
+constexpr int kLinearRows = 4;
+hipError_t launch_product_rows(const Product& g, int dtype, hipStream_t s);
+// Those of 1 to kLinearFew rows whose operands' 16-byte chunks are whole (moe_linear_few.hip).  Beyond, x costs more than the tiles'
+// idle rows: 4096 x 7168, weight by row, 16 rows 21.8 against 23.6 us, 32 rows 24.4 and 24.9, 48 rows 27.5 and 25.8.
+constexpr int kLinearFew = 32;
+int few_splits(int64_t M, int64_t N, int64_t K, bool strided);
+hipError_t launch_product_few(Product g, int dtype, void* part, hipStream_t s);
+// Adds the partial sums of g.splits and finishes y.
+hipError_t launch_product_join(const Product& g, int dtype, hipStream_t s);
 
 __device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + expf(-z)); }
 __device__ __forceinline__ float gelu_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678118654752f)); }

@@ -8,25 +8,11 @@
 // (ds_read_b64_tr_b16) make the same fragment: no copy of a transposed operand is ever written.
 #include <type_traits>
 
-#include "moe_linear.h"
+#include "moe_linear_tile.h"
 
 namespace moe {
 
-struct Plan {
-    bool dma;
-    int tile, splits;
-};
-
 namespace {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(1))) void g_void;
-typedef __attribute__((address_space(3))) void l_void;
-typedef __attribute__((address_space(3))) s16x4 l_s16x4;
 
 template <typename T> __device__ __forceinline__ f32x16 mfma(u32x4_t a, u32x4_t b, f32x16 c);
 template <> __device__ __forceinline__ f32x16 mfma<bf16_t>(u32x4_t a, u32x4_t b, f32x16 c) {
@@ -38,20 +24,6 @@ template <> __device__ __forceinline__ f32x16 mfma<fp16_t>(u32x4_t a, u32x4_t b,
 
 constexpr int kThreads = 256;   // four waves
 
-
-// One operand of a workgroup's tile: W virtual rows (A) or columns (B) from `first`, `count` of which exist.
-// For swiglu the virtual columns alternate G gate columns and the G up columns of the same outputs, so that a
-// wave holds both halves of its outputs.
-struct Side {
-    const uint16_t* p;
-    int64_t ld;
-    int first, count;   // real index of the first, and of one past the last
-    int g, up;          // G, and the offset of an up column; g = 0: not paired
-    __device__ __forceinline__ int real(int v) const {   // may be >= the bound, which limit() gives
-        return g ? first + v / (2 * g) * g + v % g + (v / g & 1) * up : first + v;
-    }
-    __device__ __forceinline__ int limit(int v) const { return g ? count + (v / g & 1) * up : count; }
-};
 
 // Moves the operand's 64-deep steps into an LDS slot through registers: instruction i of wave w covers the 1 KB
 // at 1024 (w + 4 i), lane l its 16 bytes at 16 l; the swizzle is applied to what the lane fetches.
@@ -86,8 +58,6 @@ template <bool S, int W> struct Loader {
 // The same straight from memory into LDS, without registers, for operands whose 16-byte chunks are aligned and whole:
 // past the last row (column) the last one is read again (its products are not stored), and past the end of the
 // reduction, a chunk of zeros.
-__device__ __align__(16) const uint32_t kZeroChunk[4] = {0, 0, 0, 0};
-
 template <bool S, int W> struct DmaLoader {
     static constexpr int NI = W / 32;
     const char* src[NI];   // this lane's 16 bytes of step 0
@@ -424,15 +394,8 @@ template <typename T, bool AS, bool BS, int TILE, bool DMA> hipError_t run_produ
     }
     const int64_t total = static_cast<int64_t>((g.M + TILE - 1) / TILE) * ((g.N + TILE - 1) / TILE) * g.splits;
     kernel<<<static_cast<unsigned>((total + 7) / 8 * 8), kThreads, lds, s>>>(g);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !g.part) return e;
-    const int64_t threads = static_cast<int64_t>(g.M) * ((g.out_cols + 7) / 8);
-    linear_join_kernel<T><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, s>>>(g);
     return hipGetLastError();
 }
-
-// Whether an operand's 16-byte chunks are aligned and whole (extent: what it has along its contiguous dimension).
-bool whole_chunks(const void* p, int64_t ld, int64_t extent) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && extent % 8 == 0; }
 
 template <typename T, bool AS, bool BS> hipError_t run_tiles(const Product& g, const Plan& plan, hipStream_t s) {
     if (plan.dma && plan.tile == 256) return run_product<T, AS, BS, 256, true>(g, s);
@@ -463,19 +426,33 @@ Plan product_plan(int64_t M, int64_t N, int64_t K, bool dma) {
 }
 
 size_t product_part_bytes(int64_t M, int64_t N, int64_t K) {   // whatever the alignment
-    const int with = product_plan(M, N, K, true).splits, without = product_plan(M, N, K, false).splits, splits = with > without ? with : without;
+    int splits = 1;
+    auto at_least = [&](int n) { splits = n > splits ? n : splits; };
+    at_least(product_plan(M, N, K, true).splits);
+    at_least(product_plan(M, N, K, false).splits);
+    if (M > 0 && M <= kLinearFew) at_least(few_splits(M, N, K, true)), at_least(few_splits(M, N, K, false));
     return splits > 1 ? static_cast<size_t>(splits) * M * N * 4 : 0;
 }
 
 hipError_t launch_product(Product g, int dtype, void* part, hipStream_t s) {
     if (g.M <= 0) return hipSuccess;
     const bool whole = whole_chunks(g.a, g.lda, g.a_strided ? g.M : g.K) && whole_chunks(g.b, g.ldb, g.b_strided ? (g.act == MOE_ACT_SWIGLU ? g.out_cols : g.N) : g.K);
+    if (!g.a_strided && whole && g.M <= kLinearFew && (g.M > 1 || g.b_strided)) return launch_product_few(g, dtype, part, s);
+    if (!g.a_strided && g.M <= kLinearRows) return launch_product_rows(g, dtype, s);
     const Plan plan = product_plan(g.M, g.N, g.K, whole);
     g.splits = plan.splits;
     const int steps = (g.K + kLinearDepth - 1) / kLinearDepth;
     g.slots = (steps + g.splits - 1) / g.splits;
     g.part = g.splits > 1 ? static_cast<float*>(part) : nullptr;
-    return dtype == MOE_BF16 ? run_layouts<bf16_t>(g, plan, s) : run_layouts<fp16_t>(g, plan, s);
+    const hipError_t e = dtype == MOE_BF16 ? run_layouts<bf16_t>(g, plan, s) : run_layouts<fp16_t>(g, plan, s);
+    return e == hipSuccess && g.part ? launch_product_join(g, dtype, s) : e;
+}
+
+hipError_t launch_product_join(const Product& g, int dtype, hipStream_t s) {
+    const int64_t blocks = (static_cast<int64_t>(g.M) * ((g.out_cols + 7) / 8) + 255) / 256;
+    if (dtype == MOE_BF16) linear_join_kernel<bf16_t><<<static_cast<unsigned>(blocks), 256, 0, s>>>(g);
+    else linear_join_kernel<fp16_t><<<static_cast<unsigned>(blocks), 256, 0, s>>>(g);
+    return hipGetLastError();
 }
 
 }  // namespace moe
