@@ -26,30 +26,62 @@ constexpr int kThreads = 256;   // four waves
 
 
 // Moves the operand's 64-deep steps into an LDS slot through registers: instruction i of wave w covers the 1 KB
-// at 1024 (w + 4 i), lane l its 16 bytes at 16 l; the swizzle is applied to what the lane fetches.
+// at 1024 (w + 4 i), lane l its 16 bytes at 16 l; the swizzle is applied to what the lane fetches.  For operands of any
+// alignment and size: a load is unconditional, where a chunk would reach past its row's end the row's last 16 bytes,
+// which are shifted into place on the way to LDS.  Only the reduction's end needs zeros: rows and columns of the tile past
+// the operand's make sums that are not stored.  Rows of less than a chunk are read by element.
 template <bool S, int W> struct Loader {
     static constexpr int NI = W / 32;   // instructions per wave and step
     Side o;
     int red, wave, lane;
-    u32x4_t r[NI];
+    bool tiny, edge;   // rows shorter than a chunk; strided: the tile reaches past the last whole chunk of a row
 
-    __device__ __forceinline__ void load(int step) {
+    __device__ __forceinline__ void setup(const Side& side, int reduction, int w, int l) {
+        o = side;
+        red = reduction;
+        wave = w;
+        lane = l;
+        const int length = S ? o.count : red;
+        tiny = length < 8;
+        edge = S && o.first + (o.g ? W / 2 : W) > o.count;
+    }
+    // row and first element (k and column where strided) of this lane's chunk
+    __device__ __forceinline__ int row_of(int i) const { return S ? (wave + 4 * i) * (64 / (W / 8)) + lane / (W / 8) : 8 * (wave + 4 * i) + (lane >> 3); }
+    __device__ __forceinline__ int chunk_at(int row) const { return S ? 8 * (lane % (W / 8) ^ ((row & 3) << 2)) : 8 * ((lane & 7) ^ ((row >> 1) & 7)); }
+
+    __device__ __forceinline__ void load(int step, u32x4_t (&r)[NI]) const {
         const bf16_t* p = reinterpret_cast<const bf16_t*>(o.p);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
+            const int row = row_of(i), at = chunk_at(row);
             if constexpr (!S) {
-                const int v = 8 * (wave + 4 * i) + (lane >> 3), c = (lane & 7) ^ ((v >> 1) & 7), k = step * kLinearDepth + 8 * c;
-                const int at = o.real(v);
-                r[i] = load_chunk<bf16_t>(p + at * o.ld + k, at < o.limit(v) ? red - k : 0);
+                const bf16_t* from = p + min(o.real(row), o.limit(row) - 1) * o.ld;
+                const int k = step * kLinearDepth + at;
+                r[i] = tiny ? load_chunk<bf16_t>(from + k, red - k) : *reinterpret_cast<const u32x4_any_t*>(from + min(k, red - 8));
             } else {
-                constexpr int CH = W / 8;   // chunks of a row
-                const int kr = (wave + 4 * i) * (64 / CH) + lane / CH, c = lane % CH ^ ((kr & 3) << 2), k = step * kLinearDepth + kr;
-                const int at = o.real(8 * c);
-                r[i] = load_chunk<bf16_t>(p + k * o.ld + at, k < red ? o.limit(8 * c) - at : 0);
+                const int c = o.real(at), end = o.limit(at);
+                const bf16_t* from = p + min(step * kLinearDepth + row, red - 1) * o.ld;
+                r[i] = tiny ? load_chunk<bf16_t>(from + c, end - c) : *reinterpret_cast<const u32x4_any_t*>(from + min(c, end - 8));
             }
         }
     }
-    __device__ __forceinline__ void store(char* slot) const {
+    __device__ __forceinline__ void store(int step, char* slot, u32x4_t (&r)[NI]) const {
+        if (!tiny && (edge || (step + 1) * kLinearDepth > red)) {   // the same for the workgroup
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int row = row_of(i), at = chunk_at(row);
+                if constexpr (!S) {
+                    r[i] = settle<bf16_t, false>(r[i], step * kLinearDepth + at, red);
+                } else {
+                    r[i] = settle<bf16_t, false>(r[i], o.real(at), o.limit(at));
+                    if (step * kLinearDepth + row >= red) r[i] = u32x4_t{0, 0, 0, 0};
+                }
+            }
+        } else if (S && tiny) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (step * kLinearDepth + row_of(i) >= red) r[i] = u32x4_t{0, 0, 0, 0};
+        }
 #pragma unroll
         for (int i = 0; i < NI; ++i) *reinterpret_cast<u32x4_t*>(slot + 1024 * (wave + 4 * i) + 16 * lane) = r[i];
     }
@@ -190,7 +222,7 @@ __device__ __forceinline__ void write_out(const Product& g, float* region, const
 }
 
 template <typename T, bool AS, bool BS, int TILE>
-__global__ __launch_bounds__(kThreads, 1) void linear_kernel(Product g) {
+__global__ __launch_bounds__(kThreads, 2) void linear_kernel(Product g) {
     extern __shared__ __align__(16) char lds[];
     constexpr int NB = TILE / 64, SLOT = lds_slot<TILE>(), HALF = TILE * 2 * kLinearDepth;
     int tm, tn, split;
@@ -199,11 +231,8 @@ __global__ __launch_bounds__(kThreads, 1) void linear_kernel(Product g) {
     const bool pair = g.act == MOE_ACT_SWIGLU;
     Loader<AS, TILE> a;
     Loader<BS, TILE> b;
-    a.o = Side{g.a, g.lda, tm * TILE, g.M, 0, 0};
-    b.o = pair ? Side{g.b, g.ldb, tn * (TILE / 2), g.out_cols, TILE / 4, g.out_cols} : Side{g.b, g.ldb, tn * TILE, g.N, 0, 0};
-    a.red = b.red = g.K;
-    a.wave = b.wave = wave;
-    a.lane = b.lane = lane;
+    a.setup(Side{g.a, g.lda, tm * TILE, g.M, 0, 0}, g.K, wave, lane);
+    b.setup(pair ? Side{g.b, g.ldb, tn * (TILE / 2), g.out_cols, TILE / 4, g.out_cols} : Side{g.b, g.ldb, tn * TILE, g.N, 0, 0}, g.K, wave, lane);
     Fragments<AS, TILE> fa;
     Fragments<BS, TILE> fb;
     fa.setup(wm * (TILE / 2), lane);
@@ -215,31 +244,40 @@ __global__ __launch_bounds__(kThreads, 1) void linear_kernel(Product g) {
     for (int mi = 0; mi < NB; ++mi)
 #pragma unroll
         for (int ni = 0; ni < NB; ++ni) acc[mi][ni] = f32x16{};
-    a.load(j0);
-    b.load(j0);
-    a.store(lds);
-    b.store(lds + HALF);
-    for (int j = j0; j < j1; ++j) {
-        char* cur = lds + (j - j0 & 1) * SLOT;
-        char* other = lds + SLOT - (j - j0 & 1) * SLOT;
-        lds_barrier();   // the step's operands are in LDS, and the last step's no longer read
-        if (j + 1 < j1) {
-            a.load(j + 1);
-            b.load(j + 1);
-        }
+    // two steps of loads in flight, in registers; two slots
+    u32x4_t ra[2][Loader<AS, TILE>::NI], rb[2][Loader<BS, TILE>::NI];
+    auto load = [&](int j, int u) {
+        a.load(j, ra[u]);
+        b.load(j, rb[u]);
+    };
+    auto store = [&](int j, int u) {
+        char* slot = lds + u * SLOT;
+        a.store(j, slot, ra[u]);
+        b.store(j, slot + HALF, rb[u]);
+    };
+    if (j0 < j1) {
+        load(j0, 0);
+        if (j0 + 1 < j1) load(j0 + 1, 1);
+        store(j0, 0);
+    }
+    for (int j = j0; j < j1; j += 2) {
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-            u32x4_t af[NB], bf[NB];
+        for (int u = 0; u < 2; ++u) {
+            if (j + u >= j1) break;   // the same for the workgroup
+            const char* cur = lds + u * SLOT;
+            lds_barrier();   // the step's operands are in LDS, and the last step's no longer read
+            if (j + u + 2 < j1) load(j + u + 2, u);
 #pragma unroll
-            for (int i = 0; i < NB; ++i) af[i] = fa.read(cur, i, kb), bf[i] = fb.read(cur + HALF, i, kb);
+            for (int kb = 0; kb < 4; ++kb) {
+                u32x4_t af[NB], bf[NB];
 #pragma unroll
-            for (int mi = 0; mi < NB; ++mi)
+                for (int i = 0; i < NB; ++i) af[i] = fa.read(cur, i, kb), bf[i] = fb.read(cur + HALF, i, kb);
 #pragma unroll
-                for (int ni = 0; ni < NB; ++ni) acc[mi][ni] = mfma<T>(af[mi], bf[ni], acc[mi][ni]);
-        }
-        if (j + 1 < j1) {
-            a.store(other);
-            b.store(other + HALF);
+                for (int mi = 0; mi < NB; ++mi)
+#pragma unroll
+                    for (int ni = 0; ni < NB; ++ni) acc[mi][ni] = mfma<T>(af[mi], bf[ni], acc[mi][ni]);
+            }
+            if (j + u + 1 < j1) store(j + u + 1, 1 - u);
         }
     }
     lds_barrier();

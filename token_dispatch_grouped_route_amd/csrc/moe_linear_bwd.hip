@@ -53,9 +53,9 @@ template <typename T> __global__ __launch_bounds__(256) void linear_slope_kernel
 
 }  // namespace
 
-// Runs of rows: what fills the chip four workgroups a CU, and at least 16 rows each.
+// Runs of rows: what fills the chip four workgroups a CU, and at least 8 rows, two a wave, each.
 int64_t slope_slots(int64_t M, int64_t N) {
-    const int64_t cap = 1024 / ((N + kSlopeColumns - 1) / kSlopeColumns), want = (M + 15) / 16;
+    const int64_t cap = 1024 / ((N + kSlopeColumns - 1) / kSlopeColumns), want = (M + 7) / 8;
     const int64_t n = want < cap ? want : cap;
     return n > 0 ? n : 1;
 }
