@@ -100,41 +100,56 @@ template <typename T> __device__ __forceinline__ void store8(void* base, int64_t
     }
 }
 
-// Eight columns n .. n + 7 of row m of C (for swiglu the gate's, and `up`, the up columns') on their way to
-// y, in fp32 up to the last rounding.  Each element of the residual is read right before its place in y is
-// written, by the same thread, so y may be the residual.
-template <typename T> __device__ __forceinline__ void linear_out(const Product& g, int64_t m, int n, float (&v)[8], float (&up)[8]) {
-    const int valid = g.out_cols - n;
-    const bool pair = g.act == MOE_ACT_SWIGLU;
-    if (g.bias) {
-        float b[8];
-        load8<T>(g.bias, n, g.bias_f32, valid, b);
+// Eight columns n .. n + 7 of C (for swiglu of the gate's and of the up's) on their way to y, in fp32 up to the last
+// rounding: what is added to every row, and a row's part.
+template <typename T> struct OutColumns {
+    float bias[8], bias_up[8];
+    int n, valid;
+    bool pair;
+    __device__ __forceinline__ void load(const Product& g, int n_) {
+        n = n_;
+        valid = g.out_cols - n;
+        pair = g.act == MOE_ACT_SWIGLU;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += b[i];
-        if (pair) {
-            load8<T>(g.bias, g.out_cols + n, g.bias_f32, valid, b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) up[i] += b[i];
+        for (int i = 0; i < 8; ++i) bias[i] = bias_up[i] = 0.0f;
+        if (g.bias) {
+            load8<T>(g.bias, n, g.bias_f32, valid, bias);
+            if (pair) load8<T>(g.bias, g.out_cols + n, g.bias_f32, valid, bias_up);
         }
     }
-    if (g.z) {
-        store8<T>(g.z, m * g.ldz + n, false, valid, v);
-        if (pair) store8<T>(g.z, m * g.ldz + g.out_cols + n, false, valid, up);
+    // Each element of the residual is read before its place in y is written, by the same thread, so y may be the residual.
+    __device__ __forceinline__ void residual(const Product& g, int64_t m, float (&r)[8]) const {
+        if (g.residual) load8<T>(g.residual, m * g.ldr + n, g.y_f32, valid, r);
     }
-    if (pair) {
+    __device__ __forceinline__ void store(const Product& g, int64_t m, float (&v)[8], float (&up)[8], const float (&r)[8]) const {
+        if (g.bias) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * sigmoid_f32(v[i]) * up[i];
-    } else if (g.act != MOE_ACT_NONE) {
+            for (int i = 0; i < 8; ++i) v[i] += bias[i], up[i] += bias_up[i];
+        }
+        if (g.z) {
+            store8<T>(g.z, m * g.ldz + n, false, valid, v);
+            if (pair) store8<T>(g.z, m * g.ldz + g.out_cols + n, false, valid, up);
+        }
+        if (pair) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_f32(g.act, v[i]);
+            for (int i = 0; i < 8; ++i) v[i] = v[i] * sigmoid_f32(v[i]) * up[i];
+        } else if (g.act != MOE_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = act_f32(g.act, v[i]);
+        }
+        if (g.residual) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += r[i];
+        }
+        store8<T>(g.y, m * g.ldy + n, g.y_f32, valid, v);
     }
-    if (g.residual) {
-        float r[8];
-        load8<T>(g.residual, m * g.ldr + n, g.y_f32, valid, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
-    }
-    store8<T>(g.y, m * g.ldy + n, g.y_f32, valid, v);
+};
+template <typename T> __device__ __forceinline__ void linear_out(const Product& g, int64_t m, int n, float (&v)[8], float (&up)[8]) {
+    OutColumns<T> out;
+    float r[8] = {};
+    out.load(g, n);
+    out.residual(g, m, r);
+    out.store(g, m, v, up, r);
 }
 
 }  // namespace moe

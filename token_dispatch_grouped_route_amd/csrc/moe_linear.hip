@@ -185,40 +185,76 @@ __device__ __forceinline__ bool tile_of(const Product& g, int tile, int& tm, int
 
 // The wave's blocks on their way out, 32 rows at a time through LDS (region: 32 rows of WIDE + 4 floats), so
 // that every lane ends up with 8 consecutive columns of a row.  For swiglu the first half of the block's columns are
-// the gate's.
-template <typename T, int NB, int MB>
-__device__ __forceinline__ void write_out(const Product& g, float* region, const f32x16 (&acc)[MB][NB], int64_t m0, int n0, int split, int lane) {
-    constexpr int WIDE = 32 * NB, PITCH = WIDE + 4;
-    const bool pair = g.act == MOE_ACT_SWIGLU;
-    const int chunks = pair ? WIDE / 16 : WIDE / 8, n = n0 + 8 * (lane % chunks);   // n: an output column
-#pragma unroll
+// the gate's.  A lane reads several of its rows, of the residual too, before the first is finished: with one wave a SIMD nothing
+// else hides those reads (a 256-wide tile's way out took as long as eight steps of its reduction).
+template <typename T, bool PAIR, int NB, int MB>
+__device__ __forceinline__ void write_blocks(const Product& g, float* region, const f32x16 (&acc)[MB][NB], int64_t m0, int n0, int split, int lane) {
+    constexpr int WIDE = 32 * NB, PITCH = WIDE + 4, CHUNKS = PAIR ? WIDE / 16 : WIDE / 8, STEP = 64 / CHUNKS, ROWS = 32 / STEP, BATCH = ROWS < 4 ? ROWS : 4;
+    const int n = n0 + 8 * (lane % CHUNKS);   // an output column
+    OutColumns<T> out;
+    if (n < g.out_cols && !g.part) out.load(g, n);
+    const float* mine = region + lane / CHUNKS * PITCH + 8 * (lane % CHUNKS);
+    // one copy of the rows' code for all blocks, and the accumulators still at fixed registers
+#pragma unroll 1
     for (int mi = 0; mi < MB; ++mi) {
         wave_sync();   // the last rows have been read
 #pragma unroll
-        for (int ni = 0; ni < NB; ++ni)
+        for (int b = 0; b < MB; ++b)
+            if (mi == b) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) region[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * PITCH + 32 * ni + (lane & 31)] = acc[mi][ni][r];
+                for (int ni = 0; ni < NB; ++ni)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) region[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * PITCH + 32 * ni + (lane & 31)] = acc[b][ni][r];
+            }
         wave_sync();
-        for (int row = lane / chunks; row < 32; row += 64 / chunks) {
-            const int64_t m = m0 + 32 * mi + row;
-            if (m >= g.M || n >= g.out_cols) continue;
-            const float* p = region + row * PITCH + 8 * (lane % chunks);
-            float v[8], up[8];
+        const int64_t m1 = m0 + 32 * mi + lane / CHUNKS;   // this lane's rows: m1, m1 + STEP, ...
+        if (n >= g.out_cols) continue;
+#pragma unroll 1
+        for (int i0 = 0; i0 < ROWS; i0 += BATCH) {
+            float v[BATCH][8], up[BATCH][8], res[BATCH][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = p[i];
-            if (pair) {
+            for (int i = 0; i < BATCH; ++i) {
+                const float4* p = reinterpret_cast<const float4*>(mine + (i0 + i) * STEP * PITCH);
+                auto get = [&](int at, float* to) {
+                    const float4 q = p[at];
+                    to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
+                };
+                get(0, v[i]);
+                get(1, v[i] + 4);
+                if (PAIR) {
+                    get(WIDE / 8, up[i]);
+                    get(WIDE / 8 + 1, up[i] + 4);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) up[i] = p[WIDE / 2 + i];
+                    for (int e = 0; e < 8; ++e) up[i][e] = 0.0f;
+                }
             }
             if (g.part) {
-                float* to = g.part + (static_cast<int64_t>(split) * g.M + m) * g.N + n;
-                store8<T>(to, 0, true, g.out_cols - n, v);
-                if (pair) store8<T>(to, g.out_cols, true, g.out_cols - n, up);
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int64_t m = m1 + (i0 + i) * STEP;
+                    if (m >= g.M) break;
+                    float* to = g.part + (static_cast<int64_t>(split) * g.M + m) * g.N + n;
+                    store8<T>(to, 0, true, g.out_cols - n, v[i]);
+                    if (PAIR) store8<T>(to, g.out_cols, true, g.out_cols - n, up[i]);
+                }
             } else {
-                linear_out<T>(g, m, n, v, up);
+                if (g.residual) {
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i)
+                        if (m1 + (i0 + i) * STEP < g.M) out.residual(g, m1 + (i0 + i) * STEP, res[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i)
+                    if (m1 + (i0 + i) * STEP < g.M) out.store(g, m1 + (i0 + i) * STEP, v[i], up[i], res[i]);
             }
         }
     }
+}
+template <typename T, int NB, int MB>
+__device__ __forceinline__ void write_out(const Product& g, float* region, const f32x16 (&acc)[MB][NB], int64_t m0, int n0, int split, int lane) {
+    if (g.act == MOE_ACT_SWIGLU) write_blocks<T, true>(g, region, acc, m0, n0, split, lane);
+    else write_blocks<T, false>(g, region, acc, m0, n0, split, lane);
 }
 
 template <typename T, bool AS, bool BS, int TILE>
@@ -355,11 +391,12 @@ template <typename T, bool AS, bool BS, int TILE> struct DmaLoop {
     __device__ __forceinline__ void run(int j0, int j1, char* __restrict__ s0, char* __restrict__ s1, f32x16 (&acc)[NB][NB]) const {
         a.issue_last(j0, s0);
         b.issue_last(j0, s0 + HALF);
-        landed();   // slot 0; its latency is paid once
-        if (j0 + 1 < j1) {
-            a.issue_last(j0 + 1, s1);
-            b.issue_last(j0 + 1, s1 + HALF);
-        }
+        __builtin_amdgcn_sched_barrier(0);
+        a.issue_last(min(j0 + 1, j1 - 1), s1);
+        b.issue_last(min(j0 + 1, j1 - 1), s1 + HALF);
+        wait_counts<2 * NI, true>();   // slot 0
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
         u32x4_t af[2][NB], bf[2][NB];
         fragments(s0, 0, af[0], bf[0]);
         // the steps whose successor two ahead is whole or, where all are, does not matter (the last one is read again)
@@ -448,19 +485,28 @@ template <typename T> hipError_t run_layouts(const Product& g, const Plan& plan,
 
 }  // namespace
 
-// Tile and splits of the reduction.
+// Tile and splits of the reduction: of all, the one of least estimated time.  A step of the reduction takes a workgroup 0.68 us alone on
+// its CU and 1.03 us beside another (128 wide), 1.75 us (256 wide, less in a last round that leaves CUs idle); without whole
+// chunks 1.3 and 1.9 us; a round of workgroups costs 3 us more, a split the join's launch and its sums' way to memory and back.  Measured: 2048 x 2048 x 2048 27.8 us in 256 tiles,
+// 35.4 with two splits; 512 x 4096 x 7168 44 us with four splits, 48 with two; 8192 x 2048 x 2048 71 us 256 wide, 76 us 128 wide.
 Plan product_plan(int64_t M, int64_t N, int64_t K, bool dma) {
     const int64_t steps = (K + kLinearDepth - 1) / kLinearDepth;
-    Plan p{dma, 128, 1};
-    if (M <= 0 || steps == 0) return p;
-    if (dma && ((M + 255) / 256) * ((N + 255) / 256) >= 200) p.tile = 256;
-    const int64_t tiles = (M + p.tile - 1) / p.tile * ((N + p.tile - 1) / p.tile), room = p.tile == 256 ? 256 : 512;
-    int64_t splits = room / tiles;
-    if (splits > steps / 8) splits = steps / 8;
-    if (splits < 1) return p;
-    const int64_t per = (steps + splits - 1) / splits;
-    p.splits = static_cast<int>((steps + per - 1) / per);   // none is empty
-    return p;
+    Plan best{dma, 128, 1};
+    if (M <= 0 || steps == 0) return best;
+    double least = 0.0;
+    for (int tile = 128; tile <= (dma ? 256 : 128); tile *= 2) {
+        const int64_t tiles = (M + tile - 1) / tile * ((N + tile - 1) / tile), room = tile == 256 ? 256 : 512;
+        for (int n = 1; n <= 16; ++n) {
+            if (n > 1 && (steps < 4 * n || tiles * n > room)) break;
+            const int64_t per = (steps + n - 1) / n, splits = (steps + per - 1) / per, rest = tiles * splits % room, full = tiles * splits / room;   // none is empty
+            const double alone = dma ? 0.68 : 1.3, both = tile == 256 ? 1.75 : dma ? 1.03 : 1.9;
+            const double last = rest == 0 ? 0.0 : tile == 256 ? both * (0.4 + 0.6 * rest / 256) : rest <= 256 ? alone : both;
+            double us = per * (full * both + last) + 3.0 * (full + (rest > 0)) + 3.0;
+            if (splits > 1) us += 4.0 + 5.2 * splits * M * N / 4.5e6;
+            if (least == 0.0 || us < least) least = us, best.tile = tile, best.splits = static_cast<int>(splits);
+        }
+    }
+    return best;
 }
 
 size_t product_part_bytes(int64_t M, int64_t N, int64_t K) {   // whatever the alignment
