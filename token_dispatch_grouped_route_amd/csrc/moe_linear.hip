@@ -115,17 +115,17 @@ template <bool S, int W> struct DmaLoader {
         // (v >> 1) & 7 and kr & 3 repeat with the instruction: a lane's k of instruction i is k0 (+ 4 i (64 / CH) where strided)
         k0 = S ? wave * (64 / (W / 8)) + lane / (W / 8) : 8 * ((lane & 7) ^ ((8 * wave + (lane >> 3)) >> 1 & 7));
     }
-    __device__ __forceinline__ void issue(int step, char* __restrict__ slot, int i) const {
-        __builtin_amdgcn_global_load_lds((g_void*)(src[i] + step * step_bytes), (l_void*)(slot + 1024 * (wave + 4 * i)), 16, 0, 0);
-    }
-    // a step that may reach past the reduction's end
-    __device__ __forceinline__ void issue_last(int step, char* slot) const {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
+    // LAST: the step may reach past the reduction's end
+    template <bool LAST> __device__ __forceinline__ void issue(int step, char* __restrict__ slot, int i) const {
+        if constexpr (LAST) {
             const int k = step * kLinearDepth + k0 + (S ? 4 * i * (64 / (W / 8)) : 0);
-            uint64_t p = reinterpret_cast<uint64_t>(k < red ? src[i] + step * step_bytes : reinterpret_cast<const char*>(kZeroChunk));
-            asm("" : "+v"(p));   // a selected address, not two loads under a branch
+            uint64_t p = reinterpret_cast<uint64_t>(src[i] + step * step_bytes);
+            asm("" : "+v"(p));   // both addresses at hand: one of them is selected, not a load under a branch each
+            p = k < red ? p : reinterpret_cast<uint64_t>(kZeroChunk);
+            asm("" : "+v"(p));
             __builtin_amdgcn_global_load_lds((g_void*)p, (l_void*)(slot + 1024 * (wave + 4 * i)), 16, 0, 0);
+        } else {
+            __builtin_amdgcn_global_load_lds((g_void*)(src[i] + step * step_bytes), (l_void*)(slot + 1024 * (wave + 4 * i)), 16, 0, 0);
         }
     }
 };
@@ -322,16 +322,19 @@ __global__ __launch_bounds__(kThreads, 2) void linear_kernel(Product g) {
                          pair ? tn * (TILE / 2) + wn * (TILE / 4) : tn * TILE + wn * (TILE / 2), split, lane);
 }
 
-// The K loop on DMA loads, two slots.  Per step, 16-deep parts 0 .. 3: each part's MFMAs run between the reads of the
-// next part's fragments.  Before part 3, when this step's slot has been read, one barrier (with every load landed):
-// then the next step's part 0 is read from the other slot and the loads of the step after it go into this one, so a
-// load has one step's time to land and nothing waits but the barrier.
+// The K loop on DMA loads, two slots.  Per step, 16-deep parts 0 .. 3, whose fragments are read two parts ahead (two of the next
+// step's during part 3).  So this step's slot has been read by the end of part 1: one barrier, and the loads of the step
+// after the next go into it during parts 2 and 3 and part 0 of the next step, spread out, since a compute unit takes in
+// 64 bytes a cycle and the waves stall where more are asked for at once (all of them within one part cost 4 to 9% of the
+// whole product).  A second barrier, with the next step's loads landed, stands before part 3.
 template <typename T, bool AS, bool BS, int TILE> struct DmaLoop {
-    static constexpr int NB = TILE / 64, HALF = TILE * 2 * kLinearDepth, NI = TILE / 32;
+    static constexpr int NB = TILE / 64, HALF = TILE * 2 * kLinearDepth, LOADS = 2 * (TILE / 32);
+    static constexpr int P2 = LOADS * 3 / 8, P3 = P2, P0 = LOADS - P2 - P3;   // loads in parts 2, 3 and 0
     DmaLoader<AS, TILE> a;
     DmaLoader<BS, TILE> b;
     Fragments<AS, TILE> fa;
     Fragments<BS, TILE> fb;
+    typedef u32x4_t Frags[4][NB];
 
     __device__ __forceinline__ void fragments(const char* __restrict__ slot, int kb, u32x4_t (&af)[NB], u32x4_t (&bf)[NB]) const {
 #pragma unroll
@@ -343,70 +346,72 @@ template <typename T, bool AS, bool BS, int TILE> struct DmaLoop {
 #pragma unroll
             for (int ni = 0; ni < NB; ++ni) acc[mi][ni] = mfma<T>(af[mi], bf[ni], acc[mi][ni]);
     }
-    // order: MFMA, fragment reads, a load, in turn
-    template <int LOADS> static __device__ __forceinline__ void interleave() {
-        constexpr int NM = NB * NB, NR = NB * ((AS ? 2 : 1) + (BS ? 2 : 1));
+    // loads FROM .. FROM + N - 1 of a step, of the two operands in turn
+    template <bool LAST, int FROM, int N> __device__ __forceinline__ void issue(int step, char* __restrict__ slot) const {
+#pragma unroll
+        for (int i = FROM; i < FROM + N; ++i) {
+            if (i % 2 == 0) a.template issue<LAST>(step, slot, i / 2);
+            else b.template issue<LAST>(step, slot + HALF, i / 2);
+        }
+    }
+    // order: an MFMA, fragment reads, a load, in turn
+    template <int READS, int LOADS_HERE> static __device__ __forceinline__ void interleave() {
+        constexpr int NM = NB * NB, NR = READS * NB * ((AS ? 2 : 1) + (BS ? 2 : 1)), RPM = (NR + NM - 1) / NM, LPM = (LOADS_HERE + NM - 1) / NM;
 #pragma unroll
         for (int i = 0; i < NM; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
 #pragma unroll
-            for (int x = 0; x * NM < NR; ++x)
-                if (x * NM + i < NR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            for (int x = 0; x < RPM; ++x)
+                if (i * RPM + x < NR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
 #pragma unroll
-            for (int x = 0; x * NM < LOADS; ++x)
-                if (x * NM + i < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            for (int x = 0; x < LPM; ++x)
+                if (i * LPM + x < LOADS_HERE) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
     }
-    static __device__ __forceinline__ void landed() {
-        __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+    template <int VM> static __device__ __forceinline__ void barrier() {   // with all but the last VM loads landed, and all reads
+        wait_counts<VM, true>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     }
-    // MAIN: the step two ahead (`ahead`, at most the last) is whole
-    template <bool MAIN> __device__ __forceinline__ void step(int j, int j1, int ahead, char* __restrict__ cur, char* __restrict__ other, u32x4_t (&af)[2][NB], u32x4_t (&bf)[2][NB],
-                                                              f32x16 (&acc)[NB][NB]) const {
-#pragma unroll
-        for (int kb = 0; kb < 3; ++kb) {
-            fragments(cur, kb + 1, af[(kb + 1) & 1], bf[(kb + 1) & 1]);
-            multiply(af[kb & 1], bf[kb & 1], acc);
-            interleave<0>();
-        }
-        landed();
-        if constexpr (MAIN) {
-#pragma unroll
-            for (int i = 0; i < NI; ++i) a.issue(ahead, cur, i), b.issue(ahead, cur + HALF, i);
-            fragments(other, 0, af[0], bf[0]);
-            multiply(af[1], bf[1], acc);
-            interleave<2 * NI>();
-        } else {
-            if (j + 2 < j1) {
-                a.issue_last(j + 2, cur);
-                b.issue_last(j + 2, cur + HALF);
-            }
-            multiply(af[1], bf[1], acc);
-            if (j + 1 < j1) fragments(other, 0, af[0], bf[0]);
-        }
+    // LAST: steps j + 1 and j + 2 may reach past the end.  Loads past the last step read that one again.
+    template <bool LAST> __device__ __forceinline__ void step(int j, int last, char* __restrict__ cur, char* __restrict__ other, Frags& af, Frags& bf, f32x16 (&acc)[NB][NB]) const {
+        issue<LAST, P2 + P3, P0>(min(j + 1, last), other);
+        fragments(cur, 2, af[2], bf[2]);
+        multiply(af[0], bf[0], acc);
+        interleave<1, P0>();
+        fragments(cur, 3, af[3], bf[3]);
+        multiply(af[1], bf[1], acc);
+        interleave<1, 0>();
+        barrier<63>();   // this slot has been read
+        issue<LAST, 0, P2>(min(j + 2, last), cur);
+        multiply(af[2], bf[2], acc);
+        interleave<0, P2>();
+        barrier<P2>();   // the next step has landed
+        issue<LAST, P2, P3>(min(j + 2, last), cur);
+        fragments(other, 0, af[0], bf[0]);
+        fragments(other, 1, af[1], bf[1]);
+        multiply(af[3], bf[3], acc);
+        interleave<2, P3>();
     }
     __device__ __forceinline__ void run(int j0, int j1, char* __restrict__ s0, char* __restrict__ s1, f32x16 (&acc)[NB][NB]) const {
-        a.issue_last(j0, s0);
-        b.issue_last(j0, s0 + HALF);
+        const int last = j1 - 1;
+        issue<true, 0, LOADS>(j0, s0);
         __builtin_amdgcn_sched_barrier(0);
-        a.issue_last(min(j0 + 1, j1 - 1), s1);
-        b.issue_last(min(j0 + 1, j1 - 1), s1 + HALF);
-        wait_counts<2 * NI, true>();   // slot 0
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        u32x4_t af[2][NB], bf[2][NB];
+        issue<true, 0, P2 + P3>(min(j0 + 1, last), s1);
+        barrier<P2 + P3>();
+        Frags af, bf;
         fragments(s0, 0, af[0], bf[0]);
-        // the steps whose successor two ahead is whole or, where all are, does not matter (the last one is read again)
-        const int whole = min(j1, a.red / kLinearDepth), main = whole == j1 ? j1 : whole - 2;
+        fragments(s0, 1, af[1], bf[1]);
+        const int main = a.red >= j1 * kLinearDepth ? j1 : last - 2;   // steps before it load whole ones only
         int j = j0;
         for (; j + 1 < main; j += 2) {
-            step<true>(j, j1, min(j + 2, whole - 1), s0, s1, af, bf, acc);
-            step<true>(j + 1, j1, min(j + 3, whole - 1), s1, s0, af, bf, acc);
+            step<false>(j, last, s0, s1, af, bf, acc);
+            step<false>(j + 1, last, s1, s0, af, bf, acc);
         }
-        for (; j < j1; ++j) step<false>(j, j1, 0, (j - j0) & 1 ? s1 : s0, (j - j0) & 1 ? s0 : s1, af, bf, acc);
+        // one copy of the code for the rest: with more, the accumulators, which fill their registers, are moved through memory where
+        // the paths meet
+        for (; j < j1; ++j) step<true>(j, last, (j - j0) & 1 ? s1 : s0, (j - j0) & 1 ? s0 : s1, af, bf, acc);
     }
 };
 
@@ -430,7 +435,7 @@ __global__ __launch_bounds__(kThreads, TILE == 256 ? 1 : 2) void linear_dma_kern
 #pragma unroll
         for (int ni = 0; ni < NB; ++ni) acc[mi][ni] = f32x16{};
     if (j0 < j1) loop.run(j0, j1, lds, lds + lds_slot<TILE>(), acc);
-    DmaLoop<T, AS, BS, TILE>::landed();
+    DmaLoop<T, AS, BS, TILE>::template barrier<0>();   // no load is on its way into LDS, and all has been read
     constexpr int REGION = 32 * (32 * NB + 4);
     write_out<T, NB, NB>(g, reinterpret_cast<float*>(lds) + wave * REGION, acc, static_cast<int64_t>(tm) * TILE + wm * (TILE / 2),
                          pair ? tn * (TILE / 2) + wn * (TILE / 4) : tn * TILE + wn * (TILE / 2), split, lane);
