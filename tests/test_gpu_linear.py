@@ -252,6 +252,24 @@ def test_rows_are_independent():
             assert not torch.isfinite(y[M // 2]).all()
 
 
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", BOTH)
+def test_each_gradient_alone(act, dtype):
+    """Each gradient asked for by itself has the bits that it has among all three."""
+    g = gen(15)
+    for M, K, N in ((1, 64, 40), (37, 72, 24), (200, 256, 320)):
+        x, w, b, _ = make(M, K, N, dtype, act, g, "kn", dtype)
+        dy = normal(g, M, N).to(dtype)
+        z = moe.linear_forward(x, w, b, act, keep=True)[1]
+        whole = moe.linear_backward(dy, x, w, z, act, bias=True)
+        for i, ask in enumerate((dict(dx=True, dw=False), dict(dx=False, dw=True), dict(dx=False, dw=False, bias=True))):
+            got = moe.linear_backward(dy, x, w, z, act, **ask)
+            assert torch.equal(got[i], whole[i]) and all(t is None for j, t in enumerate(got) if j != i)
+    y = moe.linear(x, w, b.requires_grad_(), act=act)   # frozen weights, a trained bias
+    y.backward(dy)
+    assert torch.equal(b.grad, whole[2])
+
+
 def test_leading_dimensions_of_x_and_autograd():
     g = gen(13)
     x = normal(g, 3, 7, 64).half().requires_grad_()

@@ -30,7 +30,7 @@ template <typename T> __global__ __launch_bounds__(256) void linear_slope_kernel
                     dy[i] = dy[i] * up[i] * act_slope_f32(MOE_ACT_SILU, z[i]);
                     sum_up[i] += dup[i];
                 }
-                store8<T>(a.dz, m * a.lddz + a.N + n, false, valid, dup);
+                if (a.dz) store8<T>(a.dz, m * a.lddz + a.N + n, false, valid, dup);
             } else if (a.act != MOE_ACT_NONE) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dy[i] *= act_slope_f32(a.act, z[i]);
