@@ -890,9 +890,9 @@ class _Linear(torch.autograd.Function):
     """linear_forward, with linear_backward for the gradients of x, w and bias; the residual's is dy."""
 
     @staticmethod
-    def forward(ctx, x, w, bias, residual, act, out_dtype):
-        want = ctx.needs_input_grad
-        y, z = linear_forward(x, w, bias, act, residual, out_dtype, keep=want[0] or want[1] or want[2])
+    def forward(ctx, x, w, bias, residual, act, out_dtype, grad):
+        want = ctx.needs_input_grad   # also under no_grad, where z is not kept
+        y, z = linear_forward(x, w, bias, act, residual, out_dtype, keep=grad and (want[0] or want[1] or want[2]))
         ctx.save_for_backward(x, w, z)
         ctx.act, ctx.bias_dtype = act, bias.dtype if bias is not None else None
         return y
@@ -905,14 +905,14 @@ class _Linear(torch.autograd.Function):
         gx, gw, gb = (None, None, None)
         if want[0] or want[1] or want[2]:
             gx, gw, gb = linear_backward(_row_major(dy), x, w, z, ctx.act, want[2] and ctx.bias_dtype, want[0], want[1])
-        return gx, gw, gb, dy if want[3] else None, None, None
+        return gx, gw, gb, dy if want[3] else None, None, None, None
 
 
 def linear(x, w, bias=None, act=None, residual=None, out_dtype=None):
     """act(x @ w + bias) + residual, differentiable in x, w, bias and residual; arguments as for linear_forward.
     linear(h, gate, out_dtype=torch.float32) makes a router's logits, linear(h, w1, act="swiglu") and
     linear(a, w2, residual=y) are a shared expert."""
-    return _Linear.apply(x, w, bias, residual, act, out_dtype)
+    return _Linear.apply(x, w, bias, residual, act, out_dtype, torch.is_grad_enabled())
 
 
 def _vectors(x, post, gate, pre):
