@@ -173,6 +173,26 @@ def test_backward(M, K, N, layout, act, dtype):
         check_backward(normal(g, M, N).to(out), x, w, normal(g, M, C).mul(2).to(dtype) if act else None, act, bias)
 
 
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("act", [None, "gelu", "swiglu"])
+@pytest.mark.parametrize("M,K,N", [(700, 1001, 515), (300, 1537, 1032), (515, 1280, 777), (129, 4095, 260)])
+def test_sizes_that_divide_into_no_chunks(M, K, N, act, layout, dtype):
+    """Odd reductions, columns or both, large enough that the operands are copied with padded rows; between NaN."""
+    g = gen(K + N)
+    x, w, b, r = make(M, K, N, dtype, act, g, "kn", torch.float32, dtype)
+
+    def framed(t):
+        box = torch.full((t.shape[0] + 1, t.shape[1] + 3), float("nan"), dtype=t.dtype, device="cuda")
+        inner = box[:-1, :-3]
+        return inner.copy_(t)
+
+    for x, w in ((x, w if layout == "kn" else w.t().contiguous().t()), (framed(x), framed(w) if layout == "kn" else framed(w.t()).t())):
+        y, z = check_forward(x, w, b, act, r)
+        assert torch.equal(y, moe.linear_forward(x, w, b, act, r)[0])
+        check_backward(normal(g, M, N).to(dtype), x, w, z, act, dtype)
+
+
 def test_backward_against_differences():
     """d sum(y v) along random directions of x, w, bias and residual, by central differences of the 64-bit formula at
     the run's own inputs: the sum of gradient times direction, within the gradients' rounding (bf16, 2^-9 each of a

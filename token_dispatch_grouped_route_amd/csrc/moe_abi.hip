@@ -693,17 +693,28 @@ LinearSizes linear_sizes(int32_t act, int32_t M, int32_t N, int32_t K, bool back
     return s;
 }
 int64_t dz_row(int64_t C) { return (C + 7) / 8 * 8; }
-// The backward's workspace: dz, then the partial rows of db, then the products' partial sums.
+// The backward's workspace: dz, then the partial rows of db, then the products' partial sums and padded copies.
 size_t dz_bytes(const LinearSizes& s) { return align_up(static_cast<size_t>(s.M) * dz_row(s.C) * 2); }
 size_t db_bytes(const LinearSizes& s) { return align_up(static_cast<size_t>(slope_slots(s.M, s.N)) * s.C * 4); }
 size_t larger(size_t a, size_t b) { return a > b ? a : b; }
+// Room for the products' padded copies, whatever the weight's layout: of x and w in the forward (not of paired rows), of w for dx and x for dw.
+size_t forward_pad_bytes(const LinearSizes& s) {
+    const int64_t x = padded_elements(s.M, s.K), by_row = s.C != s.N ? 0 : padded_elements(s.K, s.C), by_column = padded_elements(s.C, s.K);
+    return larger(product_pad_bytes(s.M, s.C, s.K, x, by_row), product_pad_bytes(s.M, s.C, s.K, x, by_column));
+}
+size_t backward_pad_bytes(const LinearSizes& s) {
+    const size_t dx = larger(product_pad_bytes(s.M, s.K, s.C, 0, padded_elements(s.K, s.C)), product_pad_bytes(s.M, s.K, s.C, 0, padded_elements(s.C, s.K)));
+    return larger(dx, larger(product_pad_bytes(s.K, s.C, s.M, padded_elements(s.M, s.K), 0), product_pad_bytes(s.C, s.K, s.M, 0, padded_elements(s.M, s.K))));
+}
+size_t forward_part_bytes(const LinearSizes& s) { return align_up(product_part_bytes(s.M, s.C, s.K)); }
+size_t backward_part_bytes(const LinearSizes& s) { return align_up(larger(product_part_bytes(s.M, s.K, s.C), product_part_bytes(s.K, s.C, s.M))); }
 }  // namespace
 
 size_t moe_linear_workspace_bytes(int32_t act, int32_t M, int32_t N, int32_t K, int32_t backward) {
     const LinearSizes s = linear_sizes(act, M, N, K, backward != 0);
     if (!s.ok) return 0;
-    if (!backward) return align_up(product_part_bytes(s.M, s.C, s.K)) + kWsAlign;
-    return dz_bytes(s) + db_bytes(s) + align_up(larger(product_part_bytes(s.M, s.K, s.C), product_part_bytes(s.K, s.C, s.M))) + kWsAlign;
+    if (!backward) return forward_part_bytes(s) + forward_pad_bytes(s) + kWsAlign;
+    return dz_bytes(s) + db_bytes(s) + backward_part_bytes(s) + backward_pad_bytes(s) + kWsAlign;
 }
 
 int32_t moe_linear_forward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_t act, int32_t M, int32_t N, int32_t K,
@@ -716,7 +727,7 @@ int32_t moe_linear_forward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_
         (z && bad_ld(ldz, M, s.C)))
         return MOE_ERR_SHAPE;
     if (M == 0) return MOE_OK;
-    const size_t need = moe_linear_workspace_bytes(act, M, N, K, 0);
+    const size_t part = forward_part_bytes(s), pad = forward_pad_bytes(s), need = part + pad + kWsAlign;
     if (!x || !w || !y || (!ws && need > kWsAlign)) return MOE_ERR_NULL;
     if (y == x || y == w || z == x || z == w || z == y || (residual == y && ldr != ldy) || (residual && residual == z)) return MOE_ERR_SHAPE;
     if (!aligned_to(x, dtype) || !aligned_to(w, dtype) || !aligned_to(bias, bdtype) || !aligned_to(residual, odtype) || !aligned_to(y, odtype) ||
@@ -729,7 +740,7 @@ int32_t moe_linear_forward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_
     g.a = static_cast<const uint16_t*>(x), g.lda = ldx, g.b = static_cast<const uint16_t*>(w), g.ldb = ldw;
     g.act = act, g.out_cols = N, g.bias = bias, g.residual = residual, g.ldr = ldr, g.y = y, g.ldy = ldy, g.z = z, g.ldz = ldz;
     g.bias_f32 = bdtype == MOE_FP32, g.y_f32 = odtype == MOE_FP32;
-    return launched(launch_product(g, dtype, ws, static_cast<hipStream_t>(stream)));
+    return launched(launch_product(g, dtype, ws, static_cast<char*>(ws) + part, pad, static_cast<hipStream_t>(stream)));
 }
 
 int32_t moe_linear_backward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_t act, int32_t M, int32_t N, int32_t K,
@@ -751,11 +762,16 @@ int32_t moe_linear_backward(int32_t dtype, int32_t bdtype, int32_t odtype, int32
     if (!aligned_to(dy, odtype) || !aligned_to(x, dtype) || !aligned_to(w, dtype) || !aligned_to(z, dtype) || !aligned_to(dx, dtype) || !aligned_to(dw, dtype) ||
         !aligned_to(dbias, bdtype) || (reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) != 0)
         return MOE_ERR_ALIGN;
-    if (ws_bytes < moe_linear_workspace_bytes(act, M, N, K, 1)) return MOE_ERR_WORKSPACE;
+    const size_t part_bytes = backward_part_bytes(s), pad_room = backward_pad_bytes(s);
+    if (ws_bytes < dz_bytes(s) + db_bytes(s) + part_bytes + pad_room + kWsAlign) return MOE_ERR_WORKSPACE;
     if (!is_gfx950()) return MOE_ERR_DEVICE;
     hipStream_t st = static_cast<hipStream_t>(stream);
     char* at = static_cast<char*>(ws);
-    const bool own_dz = (dx || dw) && (act != MOE_ACT_NONE || odtype == MOE_FP32);   // else dy is dz
+    // else dy is dz; rows that are not whole chunks are copied where that pays for a product
+    const int64_t dz_copy = padded_elements(s.M, s.C);
+    const bool own_dz = ((dx || dw) && (act != MOE_ACT_NONE || odtype == MOE_FP32)) ||
+                        (dx && dz_copy && product_pad_bytes(s.M, s.K, s.C, dz_copy, w_by_column ? padded_elements(s.C, s.K) : padded_elements(s.K, s.C)) > 0) ||
+                        (dw && dz_copy && product_pad_bytes(s.K, s.C, s.M, padded_elements(s.M, s.K), dz_copy) > 0);
     LinearSlope l = {};
     l.M = M, l.N = N, l.act = act, l.dy = dy, l.lddy = lddy, l.z = z, l.ldz = ldz, l.dy_f32 = odtype == MOE_FP32;
     l.dz = own_dz ? at : nullptr, l.lddz = dz_row(s.C);
@@ -764,14 +780,14 @@ int32_t moe_linear_backward(int32_t dtype, int32_t bdtype, int32_t odtype, int32
         const int32_t e = launched(launch_linear_slope(l, dtype, bdtype, dbias, st));
         if (e != MOE_OK) return e;
     }
-    void* part = at + dz_bytes(s) + db_bytes(s);
+    char *part = at + dz_bytes(s) + db_bytes(s), *pad = part + part_bytes;
     const uint16_t* dz = static_cast<const uint16_t*>(own_dz ? at : dy);
     const int64_t lddz = own_dz ? l.lddz : lddy;
     Product g = {};
     if (dx) {
         g.M = M, g.N = K, g.K = static_cast<int32_t>(s.C), g.a = dz, g.lda = lddz, g.b = static_cast<const uint16_t*>(w), g.ldb = ldw;
-        g.b_strided = w_by_column != 0, g.out_cols = K, g.y = dx, g.ldy = lddx;
-        const int32_t e = launched(launch_product(g, dtype, part, st));
+        g.a_padded = own_dz, g.b_strided = w_by_column != 0, g.out_cols = K, g.y = dx, g.ldy = lddx;
+        const int32_t e = launched(launch_product(g, dtype, part, pad, pad_room, st));
         if (e != MOE_OK) return e;
     }
     if (dw) {   // by column: the product's transpose, dz^T x
@@ -780,8 +796,9 @@ int32_t moe_linear_backward(int32_t dtype, int32_t bdtype, int32_t odtype, int32
         g.a_strided = g.b_strided = true, g.K = M, g.y = dw, g.ldy = lddw;
         g.M = static_cast<int32_t>(wr), g.N = g.out_cols = static_cast<int32_t>(wc);
         g.a = w_by_column ? dz : xs, g.lda = w_by_column ? lddz : ldx;
+        g.a_padded = own_dz && w_by_column, g.b_padded = own_dz && !w_by_column;
         g.b = w_by_column ? xs : dz, g.ldb = w_by_column ? ldx : lddz;
-        const int32_t e = launched(launch_product(g, dtype, part, st));
+        const int32_t e = launched(launch_product(g, dtype, part, pad, pad_room, st));
         if (e != MOE_OK) return e;
     }
     return MOE_OK;

@@ -15,6 +15,7 @@ struct Product {
     bool a_strided, b_strided;
     const uint16_t *a, *b;
     int64_t lda, ldb;
+    bool a_padded, b_padded; // its rows are followed by zeros up to a multiple of 8
     // what is done with C
     int32_t act, out_cols;   // moe_act; columns of y: N, or N / 2 for swiglu
     const void *bias, *residual;
@@ -42,7 +43,11 @@ hipError_t launch_linear_slope(const LinearSlope& a, int dtype, int bdtype, void
 
 // Bytes that launch_product may write at `part` for a product of these sizes.
 size_t product_part_bytes(int64_t M, int64_t N, int64_t K);
-hipError_t launch_product(Product g, int dtype, void* part, hipStream_t s);
+// Bytes of the padded copies of operands of a and b elements (0: none is wanted) that it makes at `pad` where that pays.
+int64_t padded_elements(int64_t rows, int64_t extent);   // 0 where extent is a multiple of 8
+size_t product_pad_bytes(int64_t M, int64_t N, int64_t K, int64_t a, int64_t b);
+// pad_bytes: room at `pad`; with less than a product's copies need it makes none.
+hipError_t launch_product(Product g, int dtype, void* part, void* pad, size_t pad_bytes, hipStream_t s);
 // The products of 1 to kLinearRows rows whose A has the reduction contiguous (moe_linear_rows.hip), without workspace.
 constexpr int kLinearRows = 4;
 hipError_t launch_product_rows(const Product& g, int dtype, hipStream_t s);

@@ -87,8 +87,8 @@ template <bool S, int W> struct Loader {
     }
 };
 
-// The same straight from memory into LDS, without registers, for operands whose 16-byte chunks are aligned and whole:
-// past the last row (column) the last one is read again (its products are not stored), and past the end of the
+// The same straight from memory into LDS, without registers, for operands whose 16-byte chunks are aligned and whole (or
+// padded with zeros): past the last row (column) the last one is read again (its products are not stored), and past the end of the
 // reduction, a chunk of zeros.
 template <bool S, int W> struct DmaLoader {
     static constexpr int NI = W / 32;
@@ -109,7 +109,7 @@ template <bool S, int W> struct DmaLoader {
             } else {
                 constexpr int CH = W / 8;
                 const int kr = (wave + 4 * i) * (64 / CH) + lane / CH, c = lane % CH ^ ((kr & 3) << 2);
-                src[i] = p + 2 * (kr * o.ld + min(o.real(8 * c), o.limit(8 * c) - 8));
+                src[i] = p + 2 * (kr * o.ld + min(o.real(8 * c), (o.limit(8 * c) + 7) / 8 * 8 - 8));   // rows are whole or padded
             }
         }
         // (v >> 1) & 7 and kr & 3 repeat with the instruction: a lane's k of instruction i is k0 (+ 4 i (64 / CH) where strided)
@@ -463,6 +463,22 @@ template <typename T> __global__ __launch_bounds__(256) void linear_join_kernel(
     linear_out<T>(g, m, n, v, up);
 }
 
+// Copies an operand's rows with zeros up to a multiple of 8 elements, 8 a thread.
+struct PadCopy {
+    const uint16_t* from;
+    uint16_t* to;
+    int64_t rows, ld;
+    int32_t extent;
+};
+__global__ __launch_bounds__(256) void linear_pad_kernel(PadCopy a, PadCopy b) {
+    const PadCopy c = blockIdx.y ? b : a;
+    const int chunks = (c.extent + 7) / 8;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = at / chunks;
+    if (row >= c.rows) return;
+    const int i = static_cast<int>(at - row * chunks) * 8;
+    *reinterpret_cast<u32x4_t*>(c.to + at * 8) = load_chunk<bf16_t>(reinterpret_cast<const bf16_t*>(c.from) + row * c.ld + i, c.extent - i);
+}
+
 template <typename T, bool AS, bool BS, int TILE, bool DMA> hipError_t run_product(const Product& g, hipStream_t s) {
     void (*kernel)(Product);
     if constexpr (DMA) kernel = &linear_dma_kernel<T, AS, BS, TILE>;
@@ -496,7 +512,7 @@ template <typename T> hipError_t run_layouts(const Product& g, const Plan& plan,
 // 35.4 with two splits; 512 x 4096 x 7168 44 us with four splits, 48 with two; 8192 x 2048 x 2048 71 us 256 wide, 76 us 128 wide.
 Plan product_plan(int64_t M, int64_t N, int64_t K, bool dma) {
     const int64_t steps = (K + kLinearDepth - 1) / kLinearDepth;
-    Plan best{dma, 128, 1};
+    Plan best{dma, 128, 1, 0.0};
     if (M <= 0 || steps == 0) return best;
     double least = 0.0;
     for (int tile = 128; tile <= (dma ? 256 : 128); tile *= 2) {
@@ -511,6 +527,7 @@ Plan product_plan(int64_t M, int64_t N, int64_t K, bool dma) {
             if (least == 0.0 || us < least) least = us, best.tile = tile, best.splits = static_cast<int>(splits);
         }
     }
+    best.us = least;
     return best;
 }
 
@@ -523,11 +540,43 @@ size_t product_part_bytes(int64_t M, int64_t N, int64_t K) {   // whatever the a
     return splits > 1 ? static_cast<size_t>(splits) * M * N * 4 : 0;
 }
 
-hipError_t launch_product(Product g, int dtype, void* part, hipStream_t s) {
+int64_t padded_elements(int64_t rows, int64_t extent) { return extent % 8 == 0 ? 0 : rows * ((extent + 7) / 8 * 8); }
+namespace {
+size_t pad_bytes_of(int64_t elements) { return (static_cast<size_t>(elements) * 2 + 255) / 256 * 256; }
+}  // namespace
+
+// Where the sizes divide into no chunks, the operands are copied with whole ones if that and the faster loop are estimated to
+// take less: a launch, and the copy at 4.5 TB/s.  8192 x 4095 x 7167 bf16 847 -> 497 us, 2047 x 2047 x 2047 50 -> 34 us.
+size_t product_pad_bytes(int64_t M, int64_t N, int64_t K, int64_t a, int64_t b) {
+    constexpr int64_t kMost = int64_t(1) << 33;   // the copy's grid stays below 2^32 threads
+    if (M <= 0 || a + b == 0 || a > kMost || b > kMost) return 0;
+    const double copy = 4.0 + 4.0 * static_cast<double>(a + b) / 4.5e6;
+    return product_plan(M, N, K, true).us + copy < product_plan(M, N, K, false).us ? pad_bytes_of(a) + pad_bytes_of(b) : 0;
+}
+
+hipError_t launch_product(Product g, int dtype, void* part, void* pad, size_t pad_bytes, hipStream_t s) {
     if (g.M <= 0) return hipSuccess;
-    const bool whole = whole_chunks(g.a, g.lda, g.a_strided ? g.M : g.K) && whole_chunks(g.b, g.ldb, g.b_strided ? (g.act == MOE_ACT_SWIGLU ? g.out_cols : g.N) : g.K);
+    const bool paired = g.b_strided && g.act == MOE_ACT_SWIGLU;   // a row of the weight is two
+    const int64_t a_rows = g.a_strided ? g.K : g.M, b_rows = g.b_strided ? g.K : g.N, a_extent = g.a_strided ? g.M : g.K, b_extent = g.b_strided ? (paired ? g.out_cols : g.N) : g.K;
+    auto ready = [](const void* p, int64_t ld, int64_t extent, bool padded) { return whole_chunks(p, ld, padded ? 0 : extent); };
+    const bool a_ready = ready(g.a, g.lda, a_extent, g.a_padded), b_ready = ready(g.b, g.ldb, b_extent, g.b_padded);
+    bool whole = a_ready && b_ready;
     if (!g.a_strided && whole && g.M <= kLinearFew && (g.M > 1 || g.b_strided)) return launch_product_few(g, dtype, part, s);
     if (!g.a_strided && g.M <= kLinearRows) return launch_product_rows(g, dtype, s);
+    if (!whole) {
+        const int64_t a = a_ready ? 0 : padded_elements(a_rows, a_extent), b = b_ready || paired ? 0 : padded_elements(b_rows, b_extent);
+        const size_t need = (a_ready || a) && (b_ready || b) ? product_pad_bytes(g.M, g.N, g.K, a, b) : 0;
+        if (need > 0 && need <= pad_bytes) {
+            PadCopy ca = {}, cb = {};
+            if (a) ca = {g.a, static_cast<uint16_t*>(pad), a_rows, g.lda, static_cast<int32_t>(a_extent)}, g.a = ca.to, g.lda = a / a_rows;
+            if (b) cb = {g.b, reinterpret_cast<uint16_t*>(static_cast<char*>(pad) + pad_bytes_of(a)), b_rows, g.ldb, static_cast<int32_t>(b_extent)}, g.b = cb.to, g.ldb = b / b_rows;
+            const int64_t chunks = (a > b ? a : b) / 8;
+            linear_pad_kernel<<<dim3(static_cast<unsigned>((chunks + 255) / 256), a && b ? 2 : 1), 256, 0, s>>>(a ? ca : cb, cb);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            whole = true;
+        }
+    }
     const Plan plan = product_plan(g.M, g.N, g.K, whole);
     g.splits = plan.splits;
     const int steps = (g.K + kLinearDepth - 1) / kLinearDepth;

@@ -15,7 +15,7 @@ template <typename T> __global__ __launch_bounds__(256) void linear_slope_kernel
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = blockIdx.x * kSlopeColumns + 8 * lane, valid = a.N - n;
     const bool pair = a.act == MOE_ACT_SWIGLU;
     float sum[8] = {}, sum_up[8] = {};
-    const int64_t per = (a.M + gridDim.y - 1) / gridDim.y, m1 = min(static_cast<int64_t>(a.M), (blockIdx.y + 1) * per);
+    const int64_t cols = pair ? 2 * static_cast<int64_t>(a.N) : a.N, per = (a.M + gridDim.y - 1) / gridDim.y, m1 = min(static_cast<int64_t>(a.M), (blockIdx.y + 1) * per);
     if (valid > 0) {
         for (int64_t m = blockIdx.y * per + wave; m < m1; m += 4) {
             float dy[8], z[8];
@@ -37,14 +37,17 @@ template <typename T> __global__ __launch_bounds__(256) void linear_slope_kernel
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum[i] += dy[i];
-            if (a.dz) store8<T>(a.dz, m * a.lddz + n, false, valid, dy);
+            if (a.dz) {
+                store8<T>(a.dz, m * a.lddz + n, false, valid, dy);
+                // zeros up to the row's end, a multiple of 8
+                for (int64_t c = cols; valid <= 8 && c < a.lddz; ++c) static_cast<T*>(a.dz)[m * a.lddz + c] = from_f32<T>(0.0f);
+            }
         }
     }
     if (!a.part) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) join[wave][8 * lane + i] = sum[i], join[wave][kSlopeColumns + 8 * lane + i] = sum_up[i];
     __syncthreads();
-    const int64_t cols = pair ? 2 * static_cast<int64_t>(a.N) : a.N;
     for (int c = threadIdx.x; c < (pair ? 2 : 1) * kSlopeColumns; c += 256) {
         const int at = blockIdx.x * kSlopeColumns + c % kSlopeColumns;
         if (at < a.N) a.part[blockIdx.y * cols + c / kSlopeColumns * a.N + at] = join[0][c] + join[1][c] + join[2][c] + join[3][c];

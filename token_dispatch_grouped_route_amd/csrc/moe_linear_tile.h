@@ -8,6 +8,7 @@ namespace moe {
 struct Plan {
     bool dma;
     int tile, splits;
+    double us;   // estimated
 };
 
 namespace {
