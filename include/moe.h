@@ -503,7 +503,8 @@ size_t moe_linear_workspace_bytes(int32_t act, int32_t M, int32_t N, int32_t K, 
  * reduction is added in a fixed order: the same bits on every run.
  * M 0 .. 2^24 (0: nothing is done), N 1 .. 2^20, K 1 .. 2^20, and at most 2^23 tiles of 128 x 128 in any product
  * (M x C; in the backward also M x K and K x C).  Pointers need their element's alignment only; with 16-byte
- * alignment, and sizes and leading dimensions that are multiples of 8, the large products run on a faster path.
+ * alignment, and sizes and leading dimensions that are multiples of 8, the products run on a faster path; operands of other
+ * sizes are first copied into ws where that pays.
  * y and z must not overlap x, w, each other or (but for y = residual) the residual.  ws [device] 256-B aligned
  * scratch, which calls in flight at the same time (and graphs replayed at the same time) must not share.
  */
