@@ -177,8 +177,13 @@ template <bool L1, int NB, int MT, int KS> hipError_t run_few(const FewExperts& 
 
 hipError_t launch_few(const FewExperts& a, hipStream_t s) {
     if (a.T <= 0) return hipSuccess;
-    hipError_t e = run_few<true, 2, 1, 4>(a, s);
-    if (e == hipSuccess) e = run_few<false, 1, 1, 4>(a, s);
+    // Waves a workgroup: four, or two for a short reduction, of which a wave of four has only a few steps, in L1 while its grid is
+    // resident at once.  Whole layer in us, four against two waves: 1 token of 6 experts, 2048 / 1408, 29.5 and 26.7; 128 tokens of 4 of 32, 2048 / 768,
+    // 67 and 62; but 16 tokens of 6 of 64, 2048 / 1408, L1 152 and 157; 1 token of one expert, 7168 / 2048, L1 27.8 and 34; I of 8192, L2 29 and 35.
+    constexpr int kShort = 2048, kResident = 1024;
+    const int64_t rows = static_cast<int64_t>(a.T) * a.k < a.EL ? a.T * a.k : a.EL;
+    hipError_t e = a.H <= kShort && rows * (a.I / 32) <= kResident ? run_few<true, 2, 1, 2>(a, s) : run_few<true, 2, 1, 4>(a, s);
+    if (e == hipSuccess) e = a.I <= kShort ? run_few<false, 1, 1, 2>(a, s) : run_few<false, 1, 1, 4>(a, s);
     if (e != hipSuccess) return e;
     few_finish_kernel<<<dim3((a.H / 4 + 255) / 256, a.T), 256, 0, s>>>(a);
     return hipGetLastError();
