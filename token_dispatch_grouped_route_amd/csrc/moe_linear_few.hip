@@ -4,7 +4,7 @@
 // A workgroup takes a few columns and its waves split the reduction.  A wave streams its own slices of the weight through its own two 4 KB LDS slots (no barrier), rows of 128
 // bytes as they are in memory: 64 columns x 32 k where columns are contiguous, read transposed (ds_read_b64_tr_b16), or
 // 32 columns x 64 k where k is.  They meet x, whose rows come from the caches, in the 16 x 16 x 32 MFMA; the waves' sums are
-// added through LDS in wave order.
+// added through LDS in wave order.  One row, 7168 x 4096 bf16 by row: 15.3 us (3.8 TB/s), and 3.9 for the join of four splits.
 #include <type_traits>
 
 #include "moe_linear_tile.h"
