@@ -518,7 +518,7 @@ int32_t moe_linear_forward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_
  * MOE_ACT_NONE): dz = dy act'(z), formed in fp32 and rounded to dtype for the products (relu's slope at 0 is 0), and
  *   dx = dz W^T   dtype [M, K] (lddx)       dw = x^T dz   dtype, laid out as w (lddw)
  *   dbias = the sum over the rows of dz before that rounding   bdtype [C]
- * each of which may be NULL, not all.  The residual's gradient is dy.  M = 0 writes zeros to dw and dbias.
+ * each of which may be NULL, not all (with M = 0 all).  The residual's gradient is dy.  M = 0 writes zeros to dw and dbias.
  * x is read for dw only, w for dx only.
  */
 int32_t moe_linear_backward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_t act, int32_t M, int32_t N, int32_t K,

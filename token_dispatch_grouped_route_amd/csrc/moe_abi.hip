@@ -753,8 +753,8 @@ int32_t moe_linear_backward(int32_t dtype, int32_t bdtype, int32_t odtype, int32
     if (bad_ld(lddy, M, N) || (dw && (bad_ld(ldx, M, K) || bad_ld(lddw, wr, wc))) || (dx && (bad_ld(ldw, wr, wc) || bad_ld(lddx, M, K))) ||
         (act != MOE_ACT_NONE && bad_ld(ldz, M, s.C)))
         return MOE_ERR_SHAPE;
+    if (M == 0 && !dw && !dbias) return MOE_OK;   // an empty dx may be NULL
     if (!dx && !dw && !dbias) return MOE_ERR_NULL;
-    if (M == 0 && !dw && !dbias) return MOE_OK;
     if (!ws || (M > 0 && (!dy || (dw && !x) || (dx && !w) || (act != MOE_ACT_NONE && !z)))) return MOE_ERR_NULL;
     const void* in[4] = {dy, x, w, z};
     for (const void* p : in)
