@@ -561,7 +561,7 @@ size_t moe_block_norm_workspace_bytes(int32_t dtype, int64_t rows, int32_t cols,
  *   dp = scale gate t                     db = N'(dp post_weight), else dp    dtype [rows, cols] (lddb)
  *   dgate [gate_rows, cols] = sum over its rows of scale t p;  dpost_weight = sum dp N(b);  dpost_bias = sum dp;
  *   dpre_weight = sum dn N(r);  dpre_bias = sum dn                            wdtype
- * summed in fp32 in an order that the sizes fix.  Each gradient may be NULL, not all.  r and the pre norm's statistics
+ * summed in fp32 in an order that the sizes fix.  Each gradient may be NULL, not all (without rows all).  r and the pre norm's statistics
  * are read only with dn; b only with MOE_POST_NORM or for dgate.  rows = 0 writes zeros to the vectors' gradients (gate_rows
  * then counts the gate's rows alone).  ws [device] 256-B aligned scratch of moe_block_norm_workspace_bytes bytes that no
  * other call in flight may share.  dx and db must not overlap an input.

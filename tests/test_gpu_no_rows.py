@@ -27,3 +27,19 @@ def test_linear(act, out):
     x, w = rows_of_none(), w.clone().requires_grad_()
     moe.linear(x, w, bias, act=act).sum().backward()
     assert x.grad.shape == x.shape and w.grad.shape == w.shape and not w.grad.any()
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True), (False, False)])
+def test_block_norm(kind, stream, post, pre):
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    gate = torch.ones(2, 64, dtype=torch.bfloat16, device="cuda")
+    for learns in (False, True):
+        x, b = rows_of_none(stream, 2), rows_of_none(torch.bfloat16, 2)
+        v = [t.clone().requires_grad_(learns) if t is not None else None for t in (gate, w if post else None, w if pre else None)]
+        r, n = moe.block_norm(x, b, v[0], post_weight=v[1], pre_weight=v[2], kind=kind, post=post, pre=pre)
+        (r.sum().float() + (n.sum().float() if pre else 0)).backward()
+        assert x.grad.shape == x.shape and x.grad.dtype == stream and b.grad.shape == b.shape
+        for t in v:
+            assert t is None or not learns or (t.grad.shape == t.shape and not t.grad.any())

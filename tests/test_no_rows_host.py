@@ -17,3 +17,18 @@ def test_linear_backward():
     assert linear_bwd(1, dy=A, x=A) == NULL          # rows, but no gradient is asked for
     assert linear_bwd(0, dw=A) == NULL               # zeros for dw need a workspace
     assert linear_bwd(0, 5) == SHAPE and linear_bwd(-1) == SHAPE
+
+
+def block_bwd(rows, parts=3, dr=None, dn=None, b=None, stats=(None, None, None, None), dx=None, db=None, vec=(None,) * 5, ws=None, n=0, w=A, gate_rows=0):
+    w1, w2 = (w if parts & 1 else None), (w if parts & 2 else None)
+    return moe.lib().moe_block_norm_backward(1, parts, 0, 0, 0, rows, 64, dr, 64, dn, 64, dr, 64, b, 64, 1.0, 1.0, w1, None, w if gate_rows else None, gate_rows, w2, *stats, dx, 64,
+                                             db, 64, *vec, ws, n, None)
+
+
+def test_block_norm_backward():
+    for parts in range(4):
+        for gate_rows in (0, 1, 2):
+            assert block_bwd(0, parts, gate_rows=gate_rows) == OK
+    assert block_bwd(2, dr=A, dn=A, b=A, stats=(None, A, None, A)) == NULL   # rows, but no gradient is asked for
+    assert block_bwd(0, vec=(None, A, None, None, None)) == NULL            # zeros for a vector need a workspace
+    assert block_bwd(0, 4) == SHAPE and block_bwd(-1) == SHAPE

@@ -876,8 +876,8 @@ int32_t moe_block_norm_backward(int32_t kind, int32_t parts, int32_t dtype, int3
     if ((!a.pre && (dn || dpre_weight || dpre_bias)) || (!a.post && (dpost_weight || dpost_bias)) || (!a.layer && (dpre_bias || dpost_bias)) || (dgate && !gate))
         return MOE_ERR_SHAPE;
     const bool vectors = dgate || dpost_weight || dpost_bias || dpre_weight || dpre_bias;
+    if (rows == 0 && !vectors) return MOE_OK;   // empty dx and db may be NULL
     if (!dx && !db && !vectors) return MOE_ERR_NULL;
-    if (rows == 0 && !vectors) return MOE_OK;
     if (!ws || (rows > 0 && ((!dr && !dn) || (dn && (!r || !pre_rstd || (a.layer && !pre_mean))) || (needs_b && !b) ||
                              (a.post && (!post_rstd || (a.layer && !post_mean))))))
         return MOE_ERR_NULL;
