@@ -385,7 +385,7 @@ size_t moe_norm_workspace_bytes(int32_t dtype, int64_t rows, int32_t cols);
  * Backward of moe_norm_forward: with xh = (x - mean) rstd and g = dy weight,
  *   dx      = rstd (g - [layer norm: sum g / cols] - xh sum (g xh) / cols)   dtype [rows, cols]
  *   dweight = sum over the rows of dy xh,  dbias = sum over the rows of dy   wdtype [cols]
- * summed in fp32 in an order that the sizes fix.  dx, dweight and dbias may each be NULL, not all; dbias
+ * summed in fp32 in an order that the sizes fix.  dx, dweight and dbias may each be NULL, not all (without rows all); dbias
  * is for layer norm only (MOE_ERR_SHAPE).  rows == 0 writes zeros to dweight and dbias.  mean (layer
  * norm) and rstd as the forward wrote them.  ws [device], moe_norm_workspace_bytes bytes, 256-B
  * aligned, is scratch that no other call in flight may share; it may be NULL when neither dweight nor dbias is asked for.  dx must not overlap

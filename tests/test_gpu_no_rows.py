@@ -43,3 +43,12 @@ def test_block_norm(kind, stream, post, pre):
         assert x.grad.shape == x.shape and x.grad.dtype == stream and b.grad.shape == b.shape
         for t in v:
             assert t is None or not learns or (t.grad.shape == t.shape and not t.grad.any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_row_norm(dtype):
+    w = torch.ones(64, dtype=dtype, device="cuda")
+    for norm in (lambda x: moe.rms_norm(x, w), lambda x: moe.layer_norm(x, w, w), lambda x: moe.layer_norm(x)):
+        x = rows_of_none(dtype)
+        norm(x).sum().backward()
+        assert x.grad.shape == x.shape and x.grad.dtype == dtype

@@ -32,3 +32,15 @@ def test_block_norm_backward():
     assert block_bwd(2, dr=A, dn=A, b=A, stats=(None, A, None, A)) == NULL   # rows, but no gradient is asked for
     assert block_bwd(0, vec=(None, A, None, None, None)) == NULL            # zeros for a vector need a workspace
     assert block_bwd(0, 4) == SHAPE and block_bwd(-1) == SHAPE
+
+
+def norm_bwd(rows, kind=0, dy=None, x=None, w=A, mean=None, rstd=None, dx=None, dw=None, db=None, ws=None, n=0):
+    return moe.lib().moe_norm_backward(kind, 0, 0, rows, 64, dy, 64, x, 64, w, mean, rstd, dx, 64, dw, db, ws, n, None)
+
+
+def test_norm_backward():
+    for kind in (0, 1):
+        assert norm_bwd(0, kind) == OK and norm_bwd(0, kind, w=None) == OK
+    assert norm_bwd(2, dy=A, x=A, mean=A, rstd=A) == NULL   # rows, but no gradient is asked for
+    assert norm_bwd(0, dw=A) == NULL                        # zeros for dweight need a workspace
+    assert norm_bwd(0, 2) == SHAPE and norm_bwd(-1) == SHAPE and norm_bwd(0, 1, db=A) == SHAPE

@@ -542,7 +542,7 @@ int32_t moe_norm_backward(int32_t kind, int32_t dtype, int32_t wdtype, int64_t r
     if (st != MOE_OK) return st;
     const bool layer = kind == MOE_LAYER_NORM;
     if (bad_ld(ldx, rows, cols) || bad_ld(lddy, rows, cols) || (dx && bad_ld(lddx, rows, cols)) || (!layer && dbias)) return MOE_ERR_SHAPE;
-    if (!dx && !dweight && !dbias) return MOE_ERR_NULL;
+    if (rows > 0 && !dx && !dweight && !dbias) return MOE_ERR_NULL;   // an empty dx may be NULL
     if (rows > 0 && (!x || !dy || !rstd || (layer && !mean))) return MOE_ERR_NULL;
     if (rows > 0 && (dx == x || dx == dy)) return MOE_ERR_SHAPE;   // not in place
     if (!aligned_to(x, dtype) || !aligned_to(dy, dtype) || !aligned_to(dx, dtype) || !aligned_to(weight, wdtype) || !aligned_to(dweight, wdtype) ||
