@@ -519,7 +519,8 @@ int32_t moe_linear_forward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_
  *   dx = dz W^T   dtype [M, K] (lddx)       dw = x^T dz   dtype, laid out as w (lddw)
  *   dbias = the sum over the rows of dz before that rounding   bdtype [C]
  * each of which may be NULL, not all (with M = 0 all).  The residual's gradient is dy.  M = 0 writes zeros to dw and dbias.
- * x is read for dw only, w for dx only.
+ * x is read for dw only, w for dx only.  z may hold infinities, as fp16 keeps a finite z beyond 65504: the slopes of gelu and silu, and
+ * silu at -infinity, are their limits there.
  */
 int32_t moe_linear_backward(int32_t dtype, int32_t bdtype, int32_t odtype, int32_t act, int32_t M, int32_t N, int32_t K,
                             const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,

@@ -69,7 +69,11 @@ __device__ __forceinline__ float act_f32(int act, float z) {   // not swiglu
         default: return z;
     }
 }
+// An infinite z (kept in fp16, a finite one beyond 65504) brought to 128, where expf(-z), erff and the slopes have reached their
+// limits in fp32: a slope there is 1 or 0, without infinity times 0.  NaN stays.
+__device__ __forceinline__ float at_most_128(float z) { return fabsf(z) > 128.0f ? copysignf(128.0f, z) : z; }
 __device__ __forceinline__ float act_slope_f32(int act, float z) {   // silu also for swiglu's gate
+    z = at_most_128(z);
     switch (act) {
         case MOE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
         case MOE_ACT_GELU: return gelu_cdf(z) + z * 0.39894228040143268f * expf(-0.5f * z * z);

@@ -63,7 +63,8 @@ template <typename T> __global__ __launch_bounds__(256) void linear_slope_kernel
                     rup[r].get(false, up);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        dup[i] = dy[i] * z[i] * sigmoid_f32(z[i]);
+                        const float zi = z[i] < 0.0f ? at_most_128(z[i]) : z[i];   // silu(-inf) = 0
+                        dup[i] = dy[i] * zi * sigmoid_f32(zi);
                         dy[i] = dy[i] * up[i] * act_slope_f32(MOE_ACT_SILU, z[i]);
                         sum_up[i] += dup[i];
                     }
