@@ -69,18 +69,17 @@ __device__ __forceinline__ float act_f32(int act, float z) {   // not swiglu
         default: return z;
     }
 }
-// An infinite z (kept in fp16, a finite one beyond 65504) brought to 128, where expf(-z), erff and the slopes have reached their
-// limits in fp32: a slope there is 1 or 0, without infinity times 0.  NaN stays.
-__device__ __forceinline__ float at_most_128(float z) { return fabsf(z) > 128.0f ? copysignf(128.0f, z) : z; }
+// The factor z beside a term that is 0 (or a sum that has reached its limit) in fp32 from 128 on: an infinite z, as fp16 keeps a finite
+// one beyond 65504, then gives the slope's limit and not infinity times 0.  NaN comes through the other factor, formed from z itself.
+__device__ __forceinline__ float at_most_128(float z) { return __builtin_amdgcn_fmed3f(z, -128.0f, 128.0f); }
 __device__ __forceinline__ float act_slope_f32(int act, float z) {   // silu also for swiglu's gate
-    z = at_most_128(z);
     switch (act) {
         case MOE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-        case MOE_ACT_GELU: return gelu_cdf(z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+        case MOE_ACT_GELU: return gelu_cdf(z) + at_most_128(z) * 0.39894228040143268f * expf(-0.5f * z * z);
         case MOE_ACT_NONE: return 1.0f;
         default: {
             const float s = sigmoid_f32(z);
-            return s * (1.0f + z * (1.0f - s));
+            return s * (1.0f + at_most_128(z) * (1.0f - s));
         }
     }
 }

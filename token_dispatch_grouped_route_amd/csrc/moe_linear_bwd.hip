@@ -63,8 +63,7 @@ template <typename T> __global__ __launch_bounds__(256) void linear_slope_kernel
                     rup[r].get(false, up);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float zi = z[i] < 0.0f ? at_most_128(z[i]) : z[i];   // silu(-inf) = 0
-                        dup[i] = dy[i] * zi * sigmoid_f32(zi);
+                        dup[i] = dy[i] * __builtin_amdgcn_fmed3f(z[i], -128.0f, __builtin_inff()) * sigmoid_f32(z[i]);   // silu(-inf) = 0
                         dy[i] = dy[i] * up[i] * act_slope_f32(MOE_ACT_SILU, z[i]);
                         sum_up[i] += dup[i];
                     }
