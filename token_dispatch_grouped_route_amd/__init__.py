@@ -856,31 +856,35 @@ def linear_forward(x, w, bias=None, act=None, residual=None, out_dtype=None, y=N
 def linear_backward(dy, x, w, z=None, act=None, bias=False, dx=True, dw=True, ws=None, stream=None):
     """(dx, dw, dbias) of linear_forward (moe_linear_backward), from the z that it kept.  dx, dw and bias (for dbias)
     say which are wanted; the others are None.  dw has w's dtype and layout; dbias x's dtype, or the one that bias
-    names (x's or fp32)."""
-    with _place(x, "x", stream):
-        dev = x.get_device()
-        px, ldx, M, K = _rows(x, "x")
-        pw, ldw, by_column = _matrix(w, "w", x)
+    names (x's or fp32).  x is read for dw only and may be None without it."""
+    with _place(dy, "dy", stream):
+        dev = dy.get_device()
+        if x is None and dw:
+            raise MoeError("dw needs x")
+        like = x if x is not None else w
+        if not isinstance(like, torch.Tensor) or like.get_device() != dev:
+            raise MoeError("x and w must be tensors on %s" % dy.device)
+        pw, ldw, by_column = _matrix(w, "w", like)
         code = _code(_ACT, act, "act")
-        C = w.shape[1]
-        if w.shape[0] != K or (act == "swiglu" and C % 2 != 0):
-            raise MoeError("w has the shape %s; [%d, %s] is needed" % (tuple(w.shape), K, "2N" if act == "swiglu" else "N"))
+        K, C = w.shape
+        if act == "swiglu" and C % 2 != 0:
+            raise MoeError("w has the shape %s; [K, 2N] is needed" % (tuple(w.shape),))
         N = C // 2 if act == "swiglu" else C
-        if not isinstance(dy, torch.Tensor) or dy.device != x.device:
-            raise MoeError("dy must be a tensor on %s" % x.device)
-        pdy, lddy = _rows(dy, "dy", dy, x.shape[:-1] + (N,))[:2]
+        lead = dy.shape[:-1]
+        px, ldx = _rows(x, "x", x, lead + (K,))[:2] if x is not None else (None, K)
+        pdy, lddy, M, _ = _rows(dy, "dy", dy, lead + (N,))
         if act is not None and z is None:
             raise MoeError("the backward of %s needs the z that the forward kept" % act)
-        pz, ldz = _rows(z, "z", x, x.shape[:-1] + (C,))[:2] if act is not None else (None, C)
-        bd = bias if isinstance(bias, torch.dtype) else x.dtype
-        gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx else None
-        gw = (torch.empty(C, K, dtype=x.dtype, device=x.device).t() if by_column else torch.empty(K, C, dtype=x.dtype, device=x.device)) if dw else None
-        gb = torch.empty(C, dtype=bd, device=x.device) if bias else None
+        pz, ldz = _rows(z, "z", w, lead + (C,))[:2] if act is not None else (None, C)
+        bd = bias if isinstance(bias, torch.dtype) else w.dtype
+        gx = torch.empty(lead + (K,), dtype=w.dtype, device=dy.device) if dx else None
+        gw = (torch.empty(C, K, dtype=w.dtype, device=dy.device).t() if by_column else torch.empty(K, C, dtype=w.dtype, device=dy.device)) if dw else None
+        gb = torch.empty(C, dtype=bd, device=dy.device) if bias else None
         if gx is None and gw is None and gb is None:
             return None, None, None
         nbytes = linear_workspace_bytes(M, N, K, act, True)
-        ws = _scratch(nbytes, x, ws)
-        _check(lib().moe_linear_backward(_code(_DTYPE, x.dtype, "x.dtype"), _code(_DTYPE, bd, "bias"), _code(_DTYPE, dy.dtype, "dy.dtype"), code, M, N, K,
+        ws = _scratch(nbytes, dy, ws)
+        _check(lib().moe_linear_backward(_code(_DTYPE, w.dtype, "w.dtype"), _code(_DTYPE, bd, "bias"), _code(_DTYPE, dy.dtype, "dy.dtype"), code, M, N, K,
                                          pdy, lddy, px, ldx, pw, ldw, by_column, pz, ldz, _address(gx), K, _address(gw), K if by_column else C,
                                          _address(gb), _address(ws), nbytes, _handle(dev)), "moe_linear_backward")
     return gx, gw, gb
@@ -893,7 +897,7 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, w, bias, residual, act, out_dtype, grad):
         want = ctx.needs_input_grad   # also under no_grad, where z is not kept
         y, z = linear_forward(x, w, bias, act, residual, out_dtype, keep=grad and (want[0] or want[1] or want[2]))
-        ctx.save_for_backward(x, w, z)
+        ctx.save_for_backward(x if want[1] else None, w, z)
         ctx.act, ctx.bias_dtype = act, bias.dtype if bias is not None else None
         return y
 
