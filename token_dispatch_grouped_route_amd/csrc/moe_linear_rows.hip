@@ -52,7 +52,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_rows_kernel(Product g, 
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int s = 0; s < SETS; ++s) {   // past K: row K - 1 again, times x = 0
+            for (int s = 0; s < SETS; ++s) {   // past K: row K - 1 again, which is not multiplied
                 const uint16_t* p = w + (k0 + min(i, rows - 1)) * g.ldb + s * g.out_cols;
                 wt[i][s] = chunk_of<T>(p, whole, valid);
             }
@@ -112,7 +112,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_rows_kernel(Product g, 
 // Weight by column (k contiguous): a wave takes two columns, the gate's and the up's of one output or two neighbours, and
 // walks K with 512 k a load.
 template <typename T, int ROWS>
-__global__ __launch_bounds__(256) void linear_columns_kernel(Product g, bool whole) {
+__global__ __launch_bounds__(256) void linear_columns_kernel(Product g) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const bool pair = g.act == MOE_ACT_SWIGLU;
     const int n = (static_cast<int>(blockIdx.x) * 4 + wave) * (pair ? 1 : 2);
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(256) void linear_columns_kernel(Product g, bool who
 template <typename T, int ROWS> hipError_t run_rows(const Product& g, hipStream_t s) {
     if (!g.b_strided) {
         const int per = g.act == MOE_ACT_SWIGLU ? 4 : 8;
-        linear_columns_kernel<T, ROWS><<<(g.out_cols + per - 1) / per, 256, 0, s>>>(g, true);
+        linear_columns_kernel<T, ROWS><<<(g.out_cols + per - 1) / per, 256, 0, s>>>(g);
         return hipGetLastError();
     }
     const bool whole = g.out_cols % 8 == 0;
