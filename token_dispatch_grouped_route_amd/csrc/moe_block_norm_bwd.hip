@@ -245,8 +245,8 @@ hipError_t launch_block_norm_bwd(const BlockNorm& a, int dtype, int wdtype, hipS
                 block_norm_rows_kernel<T><<<static_cast<unsigned>(a.rows < 4096 ? a.rows : 4096), 256, 0, s>>>(a, means);
                 block_norm_columns_kernel<T><<<dim3((a.cols + 511) / 512, static_cast<unsigned>(runs.runs)), 256, 0, s>>>(a, means, runs, part);
             };
-            if (dtype == MOE_FP16 || (dtype == MOE_FP32 && wdtype == MOE_FP16)) go(fp16_t{});
-            else go(bf16_t{});
+            if (dtype == MOE_FP16) go(fp16_t{});
+            else go(bf16_t{});   // also for fp32, whose vectors are fp32: no element has the 16-bit type
             e = hipGetLastError();
         }
         if (e != hipSuccess) return e;
