@@ -582,7 +582,9 @@ size_t moe_few_workspace_bytes(const moe_shape* shape);
  * Expert layer for the few tokens of a decode step, on the weights that moe_forward takes: y as moe_forward defines
  * it (SwiGLU rounded to bf16 between L1 and L2, the combine summed in fp32 in slot order, the same bits on every run), without
  * routing tables and row blocks: an expert's weights are read once per 32 of its pairs, straight into the matrix
- * instruction.  x, topk_idx, topk_w, w1p, w2p, y as for moe_forward.  T * k at most 4096, H and I at most 32768
+ * instruction.  So it is the faster form up to about 32 pairs an expert, and beyond that moe_forward is (8 experts of 7168 / 2048, each
+ * token to all: 32 tokens 154 us here and 200 there, 64 tokens 274 and 220, 512 tokens 1940 and 398), but for experts small
+ * enough that the caches hold them (8 of 2048 / 768: to about 200 pairs each).  x, topk_idx, topk_w, w1p, w2p, y as for moe_forward.  T * k at most 4096, H and I at most 32768
  * (MOE_ERR_SHAPE); shape->train must be 0; block_m is not used.  ws [device] 256-B aligned scratch, which calls in flight
  * at the same time (and graphs replayed at the same time) must not share.
  */

@@ -327,7 +327,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_kernel(Product g) {
 // after the next go into it during parts 2 and 3 and part 0 of the next step, spread out, since a compute unit takes in
 // 64 bytes a cycle and the waves stall where more are asked for at once (all of them within one part cost 4 to 9% of the
 // whole product).  A second barrier, with the next step's loads landed, stands before part 3.
-// Bound by the matrix core: 8192 x 8192 x 8192 bf16 822 us with W by row (1337 TFLOP/s), 796 by column (1381), 839 for x^T dz (1310).
+// 8192 x 8192 x 8192 bf16 824 us with W by row (1335 TFLOP/s), 806 by column (1365), 860 for x^T dz (1278).  At 8192 rows, 7168 and 4096 the matrix
+// core is busy 64% of the forward, 59% of dx and 54% of dW: 2, 3.5 and 1.75 rounds of tiles on 256 CUs, each with its own ramp and way out.
 template <typename T, bool AS, bool BS, int TILE> struct DmaLoop {
     static constexpr int NB = TILE / 64, HALF = TILE * 2 * kLinearDepth, LOADS = 2 * (TILE / 32);
     static constexpr int P2 = LOADS * 3 / 8, P3 = P2, P0 = LOADS - P2 - P3;   // loads in parts 2, 3 and 0
